@@ -34,6 +34,10 @@
  *                     optimisation; LLM Primer VI ch. 9, 9.2: EAGLE-2's
  *                     dynamic tree).
  *
+ *  tv_rotary_write, tv_decode_attention, tv_evict_cache  the cache: rows rotated
+ *                     and written into it, one new token's attention over it,
+ *                     and its eviction to a budget.
+ *
  * Ragged batches (trees of different sizes in one call) go through the
  * descriptors' node_counts; a NULL parent_idx means chains (linear
  * speculation).
@@ -81,7 +85,11 @@ typedef enum {
     TV_ERR_TIMEOUT = 7        /* device: a bounded wait ran out */
 } tv_status;
 
-typedef enum { TV_BF16 = 0, TV_F32 = 1 } tv_dtype;
+typedef enum {
+    TV_BF16 = 0,
+    TV_F32 = 1,
+    TV_F16 = 2                /* the cache calls (tv_cache_desc) only */
+} tv_dtype;
 
 /*
  * Tree attention problem.
@@ -492,6 +500,169 @@ TV_API tv_status tv_tree_select_device(int32_t batch, int32_t max_candidates, co
                                        const float *cand_prob, int32_t budget, int32_t *parent_idx,
                                        int32_t *tree_tokens, int32_t *cand_index, int32_t *node_counts,
                                        double *expected_accepted, int32_t *dev_status, void *stream);
+
+/*
+ * ---------------------------------------------------------------- the cache
+ *
+ * Three calls on the paged cache itself, for the draft model (which extends its
+ * own cache one token at a time) as much as for the target:
+ *
+ *  tv_rotary_write      a step's queries and keys are rotated by their
+ *                       positions; keys and values go into the cache, where
+ *                       tv_tree_attention and tv_decode_attention read them.
+ *  tv_decode_attention  one new token of every sequence attends to its cache;
+ *                       the attention weights can be summed up per cached token.
+ *  tv_evict_cache       keeps every KV head's cache to a budget by those sums.
+ *
+ * Their descriptor.  Strides are in elements, the same for K and V; element
+ * (block, slot, head, dim) of a cache lies at block * block_stride +
+ * slot * token_stride + head * head_stride + dim.  All three 0: the layout
+ * [num_blocks][block_size][num_kv_heads][head_dim] of the other calls.
+ * Strides times the element size, and the caches' addresses, are multiples of
+ * 16 bytes.  Elements of different (block, slot, head) must not overlap.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t num_q_heads;         /* (not used by tv_evict_cache, but checked) */
+    int32_t num_kv_heads;        /* divides num_q_heads; at most 128 query heads per KV head */
+    int32_t head_dim;            /* a multiple of 16 up to 256; tv_decode_attention: 64, 96, 128 or 256 */
+    int32_t block_size;          /* any, >= 1 */
+    int32_t max_blocks_per_seq;  /* row length of the block tables */
+    int32_t num_blocks;          /* physical blocks */
+    int32_t dtype;               /* tv_dtype: TV_BF16, TV_F16 or TV_F32 */
+    float softmax_scale;         /* 0 => 1/sqrt(head_dim) */
+    int32_t max_kv_len;          /* no kv_lens entry is larger; 0 = max_blocks_per_seq * block_size */
+    int64_t block_stride, token_stride, head_stride;
+    int64_t q_stride;            /* tv_decode_attention: elements between sequences of q; 0 = contiguous */
+    int64_t weight_stride;       /* elements between rows of the weight sums; 0 = max_blocks_per_seq * block_size */
+} tv_cache_desc;
+
+/*
+ * Attention of one new token per sequence.
+ *   q            [batch][num_q_heads][head_dim], q_stride between sequences
+ *   block_table  [batch][max_blocks_per_seq] int32
+ *   kv_lens      [batch] int32: cached tokens of each sequence, the new token's
+ *                own K and V (position kv_lens[b] - 1) among them
+ *   out          [batch][num_q_heads][head_dim] contiguous; not q
+ *   lse          [batch][num_q_heads] float32, or NULL: the natural log of the
+ *                sum of the exponentials of the scaled scores (what a caller
+ *                needs to join this result with attention over other tokens)
+ *   attn_weights [batch][num_kv_heads][weight_stride] float32, or NULL:
+ *                attn_weights[b][h][t] += the sum over the KV head's query heads
+ *                of the softmax weight of token t, for t < kv_lens[b]; the rest
+ *                of a row is left as it was.  What tv_evict_cache reads.
+ * Query head h reads KV head h / (num_q_heads / num_kv_heads).  Arithmetic is
+ * fp32; for bf16 and fp16 the softmax weights enter the product with the
+ * values as two 16-bit parts, so only `out` itself is rounded.
+ * A sequence with kv_lens[b] = 0 (padding of a batch) gets zeros and an lse
+ * of -inf, as does a row whose scores are all -inf.  A length outside
+ * [0, max_kv_len] or a block id out of range gives the sequence NaN rows, leaves
+ * its attn_weights as they were and writes TV_ERR_INVALID_ARG or
+ * TV_ERR_BLOCK_TABLE to *dev_status.  Cache slots past kv_lens[b] are not read.
+ * Workspace: tv_decode_attention_workspace_size bytes, 256-byte aligned, with
+ * the rules of tv_tree_attention's; it depends on the current device, and with
+ * weights it holds 4 bytes for every (query head, position below max_kv_len).
+ * Alignment: q and out 16 bytes, q_stride a multiple of 16 bytes.
+ */
+typedef struct {
+    int32_t grid_ctas;           /* CTAs that share the work of the batch equally, in 16-token tiles */
+    int32_t heads_per_unit;      /* query heads that one pass over a KV head's rows serves */
+    int32_t launches;            /* kernel launches per call */
+    int32_t smem_bytes;          /* dynamic shared memory per CTA */
+    size_t workspace_bytes;      /* same value as tv_decode_attention_workspace_size */
+} tv_decode_plan;
+
+TV_API tv_status tv_decode_attention_plan(const tv_cache_desc *desc, int32_t with_weights, tv_decode_plan *plan);
+
+TV_API size_t tv_decode_attention_workspace_size(const tv_cache_desc *desc, int32_t with_weights);
+
+TV_API tv_status tv_decode_attention(const tv_cache_desc *desc, const void *q, const void *paged_k,
+                                     const void *paged_v, const int32_t *block_table, const int32_t *kv_lens,
+                                     void *out, float *lse, float *attn_weights, void *workspace,
+                                     size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * Eviction by accumulated attention weight.
+ *
+ * A sequence with more than `budget` cached tokens keeps, for every KV head on its
+ * own, the first `sink` tokens, the last `recent` tokens, and of the tokens
+ * between the budget - sink - recent with the largest weights[b][h][t] (equal
+ * sums: the lower position; -0 equals +0; a NaN ranks below every number).  The
+ * kept tokens keep their order: the K and V rows of position kept[b][h][r] move
+ * to position r.  A sequence within the budget keeps everything.
+ *   weights          [batch][num_kv_heads][weight_stride] float32
+ *   dst_block_table  NULL: rows move inside the sequence's own blocks, which must
+ *                    belong to it alone and occur once in its table.  Otherwise
+ *                    [batch][max_blocks_per_seq] int32: the rows are copied to
+ *                    the positions of this table (blocks disjoint from those of
+ *                    block_table; only the entries that min(kv_lens[b], budget)
+ *                    tokens need are read), and the old blocks, which other
+ *                    sequences may share, stay as they are
+ *   weights_out      NULL, or `weights` itself, or an array of its shape that does
+ *                    not overlap it: position r gets the sum of kept[b][h][r], the
+ *                    positions from the new length up to kv_lens[b] get 0
+ *   kept             [batch][num_kv_heads][budget] int32, written: ascending,
+ *                    padded with -1
+ *   new_kv_lens      [batch] int32, written: min(kv_lens[b], budget); not kv_lens
+ * 0 <= sink, 0 <= recent, sink + recent <= budget, 1 <= budget.  max_kv_len (or the
+ * table's capacity) is at most TV_EVICT_MAX_LEN, else TV_ERR_UNSUPPORTED.  A
+ * length outside [0, max_kv_len] or a block id out of range (in either table)
+ * leaves the sequence as it was: kept all -1, new_kv_lens[b] = kv_lens[b], and
+ * TV_ERR_INVALID_ARG or TV_ERR_BLOCK_TABLE in *dev_status.  Two launches, no
+ * workspace.
+ */
+#define TV_EVICT_MAX_LEN 819200
+
+TV_API tv_status tv_evict_cache(const tv_cache_desc *desc, int32_t budget, int32_t sink, int32_t recent,
+                                void *paged_k, void *paged_v, const int32_t *block_table,
+                                const int32_t *kv_lens, const float *weights, const int32_t *dst_block_table,
+                                float *weights_out, int32_t *kept, int32_t *new_kv_lens, int32_t *dev_status,
+                                void *stream);
+
+/*
+ * Rotary positions, written into the cache.
+ *
+ * Node j of sequence b (a tree node, a chain's or a prompt's token) has its K and V
+ * row at logical position prefix_lens[b] + j.  Its queries and keys are rotated:
+ * pair i of a head, i < rotary_dim / 2, turns by the angle
+ * position[axis_of_pair[i]] * inv_freq[i]; elements from rotary_dim on pass.
+ *   q            [batch][num_nodes][num_q_heads][head_dim], or NULL (with q_out)
+ *   k, v         [batch][num_nodes][num_kv_heads][head_dim]; the strides between
+ *                nodes are q_stride, k_stride, v_stride (a slice of one fused
+ *                projection), between sequences num_nodes times that
+ *   inv_freq     [rotary_dim / 2] float32
+ *   parent_idx   as for tv_tree_attention (NULL: chains); read only without
+ *                positions
+ *   positions    [num_axes][batch][num_nodes] int32: the node's position on each
+ *                axis (time, height, width).  NULL: the position on every axis
+ *                is position_base[b] (NULL: prefix_lens[b]) plus the node's depth
+ *                in the tree, its index in a chain
+ *   q_out        [batch][num_nodes][num_q_heads][head_dim] contiguous; may be q
+ *                where that is contiguous too
+ *   paged_k/v    the caches, written; not overlapping q, k or v
+ * The angle is formed in fp64, the rotation in fp32, rounded once.
+ * Nodes at or past node_counts[b] are left alone: their q_out rows are not
+ * written.  A node count outside [0, num_nodes], a span past the table
+ * (TV_ERR_INVALID_ARG, the whole sequence), a block id out of range
+ * (TV_ERR_BLOCK_TABLE, the nodes in that block) or a malformed root path
+ * (TV_ERR_TREE, the nodes on it) gives those nodes NaN q_out rows and leaves
+ * the cache as it was there.  One launch, no workspace.
+ */
+typedef struct {
+    int32_t num_nodes;           /* nodes per sequence (capacity), >= 1; with parent_idx at most 1024 */
+    int32_t rotary_dim;          /* a multiple of 16 up to head_dim */
+    int32_t interleaved;         /* 0: pair i = elements i and i + rotary_dim / 2; 1: 2i and 2i + 1 */
+    int32_t num_axes;            /* 1..4 */
+    int64_t q_stride, k_stride, v_stride;  /* elements; 0 = contiguous */
+    const int32_t *node_counts;  /* device [batch], or NULL (= num_nodes each) */
+    uint8_t axis_of_pair[128];   /* rotary_dim / 2 entries, each below num_axes */
+} tv_rotary_desc;
+
+TV_API tv_status tv_rotary_write(const tv_cache_desc *desc, const tv_rotary_desc *rot, const void *q, const void *k,
+                                 const void *v, const float *inv_freq, const int32_t *parent_idx,
+                                 const int32_t *positions, const int32_t *position_base,
+                                 const int32_t *prefix_lens, const int32_t *block_table, void *q_out,
+                                 void *paged_k, void *paged_v, int32_t *dev_status, void *stream);
 
 /* Static string for a status code. */
 TV_API const char *tv_status_string(int32_t status);

@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libtreeverify.so")
 
 TV_OK, TV_ERR_INVALID_ARG, TV_ERR_UNSUPPORTED, TV_ERR_TREE = 0, 1, 2, 3
 TV_ERR_BLOCK_TABLE, TV_ERR_WORKSPACE, TV_ERR_CUDA, TV_ERR_TIMEOUT = 4, 5, 6, 7
-TV_BF16, TV_F32 = 0, 1
+TV_BF16, TV_F32, TV_F16 = 0, 1, 2
+TV_EVICT_MAX_LEN = 819200
 TV_STATIC_SCRATCH_BYTES = 2 << 20
 
 
@@ -45,6 +46,26 @@ class TvSampleDesc(ctypes.Structure):
 class TvSamplePlan(ctypes.Structure):
     _fields_ = [("cluster_ctas", ctypes.c_int32), ("threads", ctypes.c_int32), ("slice", ctypes.c_int32),
                 ("smem_bytes", ctypes.c_int32), ("launches", ctypes.c_int32)]
+
+
+class TvCacheDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("max_kv_len", ctypes.c_int32), ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("weight_stride", ctypes.c_int64)]
+
+
+class TvDecodePlan(ctypes.Structure):
+    _fields_ = [("grid_ctas", ctypes.c_int32), ("heads_per_unit", ctypes.c_int32), ("launches", ctypes.c_int32),
+                ("smem_bytes", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class TvRotaryDesc(ctypes.Structure):
+    _fields_ = [("num_nodes", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("node_counts", ctypes.c_void_p),
+                ("axis_of_pair", ctypes.c_uint8 * 128)]
 
 
 class TreeVerifyError(RuntimeError):
@@ -85,13 +106,22 @@ def lib() -> ctypes.CDLL:
         L.tv_tree_select_batch.argtypes = [ctypes.c_int32, P, P, P, P, ctypes.c_int32, P, P, P, P, P]
         L.tv_tree_select_device.argtypes = [ctypes.c_int32, ctypes.c_int32, P, P, P, P, ctypes.c_int32, P, P, P, P,
                                             P, P, P]
+        desc = ctypes.POINTER(TvCacheDesc)
+        L.tv_decode_attention_plan.argtypes = [desc, ctypes.c_int32, ctypes.POINTER(TvDecodePlan)]
+        L.tv_decode_attention_workspace_size.argtypes = [desc, ctypes.c_int32]
+        L.tv_decode_attention_workspace_size.restype = sz
+        L.tv_decode_attention.argtypes = [desc, P, P, P, P, P, P, P, P, P, sz, P, P]
+        L.tv_evict_cache.argtypes = [desc, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P, P, P, P, P,
+                                     P, P]
+        L.tv_rotary_write.argtypes = [desc, ctypes.POINTER(TvRotaryDesc), P, P, P, P, P, P, P, P, P, P, P, P, P, P]
         L.tv_status_string.argtypes = [ctypes.c_int32]
         L.tv_status_string.restype = ctypes.c_char_p
         L.tv_version.restype = ctypes.c_int32
         for name in ("tv_tree_attention_plan", "tv_tree_attention", "tv_tree_attention_static",
                      "tv_verify_sample_plan", "tv_verify_sample", "tv_commit_path", "tv_verify_sample_logits",
                      "tv_tree_fill_topk", "tv_tree_shape", "tv_tree_select", "tv_tree_select_batch", "tv_tree_select_device",
-                     "tv_tree_shape_for_cost", "tv_tree_merge"):
+                     "tv_tree_shape_for_cost", "tv_tree_merge", "tv_decode_attention_plan", "tv_decode_attention",
+                     "tv_evict_cache", "tv_rotary_write"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -458,3 +488,280 @@ def commit_path(k_cache, v_cache, block_table, prefix_lens, accepted_path, accep
     if s != TV_OK:
         raise TreeVerifyError(s, "tv_commit_path")
     return new_prefix_lens
+
+
+# ------------------------------------------------------------ the cache
+
+def tv_decode_attention_plan(desc: TvCacheDesc, with_weights: bool = False) -> TvDecodePlan:
+    plan = TvDecodePlan()
+    s = lib().tv_decode_attention_plan(ctypes.byref(desc), int(with_weights), ctypes.byref(plan))
+    if s != TV_OK:
+        raise TreeVerifyError(s, "tv_decode_attention_plan")
+    return plan
+
+
+def tv_decode_attention_workspace_size(desc: TvCacheDesc, with_weights: bool = False) -> int:
+    return int(lib().tv_decode_attention_workspace_size(ctypes.byref(desc), int(with_weights)))
+
+
+def tv_decode_attention(desc, q, paged_k, paged_v, block_table, kv_lens, out, lse=None, attn_weights=None,
+                        workspace=None, workspace_bytes: int = 0, dev_status=None, stream=None) -> int:
+    return int(lib().tv_decode_attention(ctypes.byref(desc), _ptr(q), _ptr(paged_k), _ptr(paged_v),
+                                         _ptr(block_table), _ptr(kv_lens), _ptr(out), _ptr(lse), _ptr(attn_weights),
+                                         _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream)))
+
+
+def tv_evict_cache(desc, budget: int, sink: int, recent: int, paged_k, paged_v, block_table, kv_lens, weights,
+                   dst_block_table, weights_out, kept, new_kv_lens, dev_status=None, stream=None) -> int:
+    return int(lib().tv_evict_cache(ctypes.byref(desc), int(budget), int(sink), int(recent), _ptr(paged_k),
+                                    _ptr(paged_v), _ptr(block_table), _ptr(kv_lens), _ptr(weights),
+                                    _ptr(dst_block_table), _ptr(weights_out), _ptr(kept), _ptr(new_kv_lens),
+                                    _ptr(dev_status), _stream(stream)))
+
+
+def tv_rotary_write(desc, rot, q, k, v, inv_freq, parent_idx, positions, position_base, prefix_lens, block_table,
+                    q_out, paged_k, paged_v, dev_status=None, stream=None) -> int:
+    return int(lib().tv_rotary_write(ctypes.byref(desc), ctypes.byref(rot), _ptr(q), _ptr(k), _ptr(v), _ptr(inv_freq),
+                                     _ptr(parent_idx), _ptr(positions), _ptr(position_base), _ptr(prefix_lens),
+                                     _ptr(block_table), _ptr(q_out), _ptr(paged_k), _ptr(paged_v), _ptr(dev_status),
+                                     _stream(stream)))
+
+
+class _Launch:
+    """The device and stream of a call on the cache: every tensor has to lie on the first
+    one's GPU, which is made current; what is allocated belongs to the stream that the
+    kernels run on (`stream`, or the GPU's current one)."""
+
+    def __init__(self, stream, first, *others):
+        import torch
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError("all tensors must be CUDA tensors")
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"all tensors must be on one GPU: {dev} and {t.device}")
+        self.guards = []
+        if torch.cuda.current_device() != dev.index:
+            self.guards.append(torch.cuda.device(dev))
+        if stream is None:
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=dev)
+            elif stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            self.stream = stream.cuda_stream
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _want(name, t, dtype, shape, optional=False):
+    """A contiguous tensor of the given type and shape."""
+    if t is None:
+        if not optional:
+            raise ValueError(f"{name} is required")
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+_cache_types: dict = {}
+
+
+def cache_desc(k_cache, v_cache, block_table, num_q_heads: int | None = None, softmax_scale: float = 0.0,
+               max_kv_len: int = 0) -> TvCacheDesc:
+    """Descriptor of a paged cache from tensors: caches [nb][block][Hkv][D] of any
+    strides with contiguous head rows (equal for K and V), block_table [B][max_blocks]
+    int32."""
+    import torch
+    if not _cache_types:
+        _cache_types.update({torch.bfloat16: TV_BF16, torch.float32: TV_F32, torch.float16: TV_F16})
+    dt = _cache_types.get(k_cache.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {k_cache.dtype}")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must be [num_blocks][block_size][num_kv_heads][head_dim] of one type")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise TypeError("block_table must be a contiguous int32 [batch][max_blocks]")
+    nb, bs, hkv, d = k_cache.shape
+    strides = (0, 0, 0)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        strides = _row_strides("k_cache", k_cache)
+        if _row_strides("v_cache", v_cache) != strides:
+            raise ValueError("k_cache and v_cache must have the same strides")
+    b, mb = block_table.shape
+    return TvCacheDesc(b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
+                       int(max_kv_len), *strides, 0, 0)
+
+
+def _row_strides(name, c):
+    """Strides of the first three dimensions of a cache (those of dimensions of size 1 say
+    nothing: the row's); the last has to be 1, and no two rows may share memory."""
+    if c.stride(3) != 1 and c.size(3) > 1:
+        raise ValueError(f"{name}: the elements of a head's row must be contiguous")
+    strides = tuple(st if n > 1 else c.size(3) for n, st in zip(c.shape[:3], c.stride()[:3]))
+    end = c.size(3)
+    for st, n in sorted(zip(strides, c.shape[:3])):
+        if n > 1:
+            if st < end:
+                raise ValueError(f"{name}: rows overlap (strides {tuple(c.stride())})")
+            end = st * (n - 1) + end
+    return strides
+
+
+def decode_attention(q, k_cache, v_cache, block_table, kv_lens, softmax_scale: float = 0.0, attn_weights=None,
+                     out=None, lse=None, workspace=None, max_kv_len: int = 0, dev_status=None, stream=None):
+    """Run tv_decode_attention: one new token per sequence, q [B][Hq][D] (sequences may lie
+    apart), over the paged cache; returns (out, lse [B][Hq] float32).  attn_weights
+    [B][Hkv][width] float32, width at least max_kv_len (default: the block table's
+    capacity), is added to in place."""
+    import torch
+    if q.dim() != 3 or q.dtype != k_cache.dtype:
+        raise TypeError("q must be [batch][heads][head_dim] of the caches' type")
+    B, Hq, D = q.shape
+    desc = cache_desc(k_cache, v_cache, block_table, Hq, softmax_scale, max_kv_len)
+    if desc.batch != B or desc.head_dim != D:
+        raise ValueError("q, block_table and the caches disagree on batch or head_dim")
+    if not q.is_contiguous():
+        if (D > 1 and q.stride(2) != 1) or (Hq > 1 and q.stride(1) != D):
+            raise ValueError("q: the heads of a sequence must be contiguous")
+        desc.q_stride = q.stride(0) if B > 1 else 0
+    _want("kv_lens", kv_lens, torch.int32, (B,))
+    if attn_weights is not None:
+        _want("attn_weights", attn_weights, torch.float32, (B, desc.num_kv_heads, attn_weights.shape[-1]))
+        desc.weight_stride = attn_weights.shape[2]
+    with _Launch(stream, q, k_cache, v_cache, block_table, kv_lens, attn_weights, out, lse, workspace,
+                 dev_status) as st:
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        else:
+            _want("out", out, q.dtype, (B, Hq, D))
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        else:
+            _want("lse", lse, torch.float32, (B, Hq))
+        if workspace is None:
+            ws_bytes = tv_decode_attention_workspace_size(desc, attn_weights is not None)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        s = tv_decode_attention(desc, q, k_cache, v_cache, block_table, kv_lens, out, lse, attn_weights, workspace,
+                                workspace.numel() * workspace.element_size(), dev_status, st)
+    if s != TV_OK:
+        raise TreeVerifyError(s, "tv_decode_attention")
+    return out, lse
+
+
+def evict_cache(k_cache, v_cache, block_table, kv_lens, weights, budget: int, sink: int = 0, recent: int = 0,
+                dst_block_table=None, weights_out=None, kept=None, new_kv_lens=None, max_kv_len: int = 0,
+                dev_status=None, stream=None):
+    """Run tv_evict_cache on the caches (in place, or into the blocks of dst_block_table);
+    returns (new_kv_lens [B], kept [B][Hkv][budget]), int32.  weights [B][Hkv][width]
+    float32; weights_out, of its shape, may be weights itself."""
+    import torch
+    desc = cache_desc(k_cache, v_cache, block_table, None, 0.0, max_kv_len)
+    B, Hkv = desc.batch, desc.num_kv_heads
+    _want("kv_lens", kv_lens, torch.int32, (B,))
+    _want("weights", weights, torch.float32, (B, Hkv, weights.shape[-1]))
+    _want("weights_out", weights_out, torch.float32, weights.shape, optional=True)
+    _want("dst_block_table", dst_block_table, torch.int32, block_table.shape, optional=True)
+    desc.weight_stride = weights.shape[2]
+    budget = int(budget)
+    with _Launch(stream, k_cache, v_cache, block_table, kv_lens, weights, dst_block_table, weights_out, kept,
+                 new_kv_lens, dev_status) as st:
+        if kept is None:
+            kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+        else:
+            _want("kept", kept, torch.int32, (B, Hkv, budget))
+        if new_kv_lens is None:
+            new_kv_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+        else:
+            _want("new_kv_lens", new_kv_lens, torch.int32, (B,))
+        s = tv_evict_cache(desc, budget, sink, recent, k_cache, v_cache, block_table, kv_lens, weights,
+                           dst_block_table, weights_out, kept, new_kv_lens, dev_status, st)
+    if s != TV_OK:
+        raise TreeVerifyError(s, "tv_evict_cache")
+    return new_kv_lens, kept
+
+
+def _node_stride(name, t):
+    """Elements between consecutive nodes of [B][N][H][D]: heads contiguous, sequences N nodes apart."""
+    B, N, H, D = t.shape
+    if t.is_contiguous():
+        return 0
+    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D):
+        raise ValueError(f"{name}: the heads of a node must be contiguous")
+    st = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else 0)
+    if B > 1 and N > 1 and t.stride(0) != N * st:
+        raise ValueError(f"{name}: sequences must lie num_nodes nodes apart")
+    return st
+
+
+def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=None, q_out=None, parent_idx=None,
+                 positions=None, position_base=None, axis_of_pair=None, interleaved: bool = False, node_counts=None,
+                 dev_status=None, stream=None):
+    """Run tv_rotary_write: rotate q [B][N][Hq][D] and k [B][N][Hkv][D], write k and v into
+    the caches at prefix_lens[b] + j; returns q_out (None without q).  inv_freq
+    [rotary_dim / 2] float32; positions [axes][B][N] int32, or None: the base
+    (position_base, else prefix_lens) plus the node's depth under parent_idx (None: chains);
+    axis_of_pair: the axis of each frequency (a sequence of rotary_dim / 2 integers; None:
+    axis 0)."""
+    import torch
+    if k.dim() != 4 or v.shape != k.shape or k.dtype != k_cache.dtype or v.dtype != k.dtype:
+        raise TypeError("k and v must be [batch][nodes][num_kv_heads][head_dim] of the caches' type")
+    B, N, Hkv, D = k.shape
+    Hq = Hkv
+    if q is not None:
+        if q.dim() != 4 or q.dtype != k.dtype or q.shape[:2] != k.shape[:2] or q.shape[3] != D:
+            raise TypeError("q must be [batch][nodes][num_q_heads][head_dim] of k's type")
+        Hq = q.shape[2]
+    desc = cache_desc(k_cache, v_cache, block_table, Hq)
+    if (desc.batch, desc.num_kv_heads, desc.head_dim) != (B, Hkv, D):
+        raise ValueError("k, block_table and the caches disagree on batch, heads or head_dim")
+    pairs = inv_freq.numel()
+    _want("inv_freq", inv_freq, torch.float32, (pairs,))
+    _want("prefix_lens", prefix_lens, torch.int32, (B,))
+    _want("position_base", position_base, torch.int32, (B,), optional=True)
+    _want("parent_idx", parent_idx, torch.int32, (B, N), optional=True)
+    _want("node_counts", node_counts, torch.int32, (B,), optional=True)
+    rot = TvRotaryDesc()
+    rot.num_nodes, rot.rotary_dim, rot.interleaved, rot.num_axes = N, 2 * pairs, int(bool(interleaved)), 1
+    if axis_of_pair is not None:
+        axes = bytes(axis_of_pair)
+        if len(axes) != pairs or pairs > 128:
+            raise ValueError("axis_of_pair must have an entry for each of inv_freq (at most 128)")
+        ctypes.memmove(rot.axis_of_pair, axes, pairs)
+        rot.num_axes = max(axes, default=0) + 1
+    if positions is not None:
+        _want("positions", positions, torch.int32, (positions.shape[0], B, N))
+        if positions.shape[0] < rot.num_axes:
+            raise ValueError("axis_of_pair names an axis that positions lacks")
+        rot.num_axes = positions.shape[0]
+    if node_counts is not None:
+        rot.node_counts = node_counts.data_ptr()
+    rot.k_stride, rot.v_stride = _node_stride("k", k), _node_stride("v", v)
+    if q is not None:
+        rot.q_stride = _node_stride("q", q)
+    with _Launch(stream, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
+                 position_base, node_counts, dev_status) as st:
+        if q is not None and q_out is None:
+            q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        elif q_out is not None:
+            _want("q_out", q_out, k.dtype, (B, N, Hq, D))
+        s = tv_rotary_write(desc, rot, q, k, v, inv_freq, parent_idx, positions, position_base, prefix_lens,
+                            block_table, q_out, k_cache, v_cache, dev_status, st)
+    if s != TV_OK:
+        raise TreeVerifyError(s, "tv_rotary_write")
+    return q_out

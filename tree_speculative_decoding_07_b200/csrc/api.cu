@@ -141,6 +141,81 @@ tv_status verify_sample_common(const tv_sample_desc* desc, const float* p, const
 }
 }  // namespace
 
+namespace {
+
+size_t elem_size(int dtype) { return dtype == TV_F32 ? 4 : 2; }
+
+int64_t cache_capacity(const tv_cache_desc* d) { return (int64_t)d->max_blocks_per_seq * d->block_size; }
+int32_t cache_max_len(const tv_cache_desc* d) {
+    return d->max_kv_len ? d->max_kv_len : (int32_t)cache_capacity(d);
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+tv_status check_cache_desc(const tv_cache_desc* d) {
+    if (!d) return TV_ERR_INVALID_ARG;
+    if (d->batch < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1 || d->head_dim < 1) return TV_ERR_INVALID_ARG;
+    if (d->num_q_heads % d->num_kv_heads) return TV_ERR_INVALID_ARG;
+    if (d->block_size < 1 || d->max_blocks_per_seq < 1 || d->num_blocks < 1) return TV_ERR_INVALID_ARG;
+    if (d->dtype != TV_BF16 && d->dtype != TV_F32 && d->dtype != TV_F16) return TV_ERR_INVALID_ARG;
+    if (!(d->softmax_scale >= 0.f) || isinf(d->softmax_scale)) return TV_ERR_INVALID_ARG;
+    if (d->num_q_heads / d->num_kv_heads > 128) return TV_ERR_UNSUPPORTED;
+    if (d->head_dim % 16 || d->head_dim > 256) return TV_ERR_UNSUPPORTED;
+    if (cache_capacity(d) > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
+    if (d->max_kv_len < 0 || d->max_kv_len > cache_capacity(d)) return TV_ERR_INVALID_ARG;
+    const bool dense = !d->block_stride && !d->token_stride && !d->head_stride;
+    if (!dense && (d->block_stride < 1 || d->token_stride < 1 || d->head_stride < 1)) return TV_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)elem_size(d->dtype);
+    if (d->block_stride * es % 16 || d->token_stride * es % 16 || d->head_stride * es % 16) return TV_ERR_INVALID_ARG;
+    if (d->weight_stride < 0 || (d->weight_stride && d->weight_stride < cache_max_len(d))) return TV_ERR_INVALID_ARG;
+    if (d->q_stride < 0 || (d->q_stride && d->q_stride < (int64_t)d->num_q_heads * d->head_dim))
+        return TV_ERR_INVALID_ARG;
+    if (d->q_stride * es % 16) return TV_ERR_INVALID_ARG;
+    if ((int64_t)d->batch * d->num_q_heads * d->head_dim > INT32_MAX) return TV_ERR_UNSUPPORTED;
+    return TV_OK;
+}
+
+tv::CacheView cache_view(const tv_cache_desc* d, const int32_t* table) {
+    const int64_t es = (int64_t)elem_size(d->dtype), row = (int64_t)d->head_dim * es;
+    const bool dense = !d->block_stride && !d->token_stride && !d->head_stride;
+    tv::CacheView c = {};
+    c.table = table;
+    c.max_blocks = d->max_blocks_per_seq;
+    c.num_blocks = d->num_blocks;
+    c.block_size = d->block_size;
+    c.head_stride = dense ? row : d->head_stride * es;
+    c.token_stride = dense ? row * d->num_kv_heads : d->token_stride * es;
+    c.block_stride = dense ? row * d->num_kv_heads * d->block_size : d->block_stride * es;
+    return c;
+}
+
+int64_t weight_stride(const tv_cache_desc* d) { return d->weight_stride ? d->weight_stride : cache_capacity(d); }
+
+// The decode call's launch and the parts of its workspace.
+struct DecodeLayout {
+    tv::DecodePlan plan;
+    size_t lse2, ml, o, scores, bytes;  // offsets; the tile counts come first
+};
+
+tv_status decode_layout(const tv_cache_desc* d, bool weights, DecodeLayout* y) {
+    tv_status s = check_cache_desc(d);
+    if (s != TV_OK) return s;
+    if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128 && d->head_dim != 256) return TV_ERR_UNSUPPORTED;
+    const int G = d->num_q_heads / d->num_kv_heads, max_len = cache_max_len(d);
+    tv::DecodePlan& p = y->plan;
+    tv::decode_plan(d->dtype, d->batch, d->num_kv_heads, G, d->head_dim, max_len, device_sms(), &p);
+    const int64_t tiles = (int64_t)d->batch * d->num_kv_heads * p.NG * ((max_len + 15) / 16);
+    if (tiles > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
+    y->lse2 = align256(sizeof(int32_t) * ((size_t)d->batch + 1));
+    y->ml = y->lse2 + (weights ? align256(sizeof(float) * (size_t)d->batch * d->num_q_heads) : 0);
+    y->o = y->ml + align256(sizeof(float) * 2 * 2 * (size_t)p.grid * p.HT);
+    y->scores = y->o + align256(sizeof(float) * 2 * (size_t)p.grid * p.HT * d->head_dim);
+    y->bytes = y->scores + (weights ? align256(sizeof(float) * (size_t)tiles * 16 * p.GS) : 0);
+    return TV_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 int32_t tv_version(void) { return 100; }
@@ -393,6 +468,117 @@ tv_status tv_verify_sample_logits(const tv_sample_desc* desc, const float* targe
     (void)workspace_bytes;
     return verify_sample_common(desc, target_logits, draft_logits, tree_tokens, parent_idx, uniforms, accepted_path,
                                 accepted_len, bonus_token, dev_status, stream, true);
+}
+
+tv_status tv_decode_attention_plan(const tv_cache_desc* desc, int32_t with_weights, tv_decode_plan* plan) {
+    DecodeLayout y;
+    tv_status s = decode_layout(desc, with_weights != 0, &y);
+    if (s != TV_OK) return s;
+    if (!plan) return TV_ERR_INVALID_ARG;
+    plan->grid_ctas = y.plan.grid;
+    plan->heads_per_unit = y.plan.HT;
+    plan->launches = y.plan.grid > 1 || with_weights ? 2 : 1;
+    plan->smem_bytes = y.plan.smem;
+    plan->workspace_bytes = y.bytes;
+    return TV_OK;
+}
+
+size_t tv_decode_attention_workspace_size(const tv_cache_desc* desc, int32_t with_weights) {
+    DecodeLayout y;
+    return decode_layout(desc, with_weights != 0, &y) == TV_OK ? y.bytes : 0;
+}
+
+tv_status tv_decode_attention(const tv_cache_desc* desc, const void* q, const void* paged_k, const void* paged_v,
+                              const int32_t* block_table, const int32_t* kv_lens, void* out, float* lse,
+                              float* attn_weights, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              void* stream) {
+    DecodeLayout y;
+    tv_status s = decode_layout(desc, attn_weights != nullptr, &y);
+    if (s != TV_OK) return s;
+    if (!q || !paged_k || !paged_v || !block_table || !kv_lens || !out || out == q) return TV_ERR_INVALID_ARG;
+    if (misaligned(q) || misaligned(paged_k) || misaligned(paged_v) || misaligned(out)) return TV_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < y.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return TV_ERR_WORKSPACE;
+    tv::DecodeArgs a = {};
+    a.q = q; a.k = paged_k; a.v = paged_v; a.c = cache_view(desc, block_table); a.lens = kv_lens;
+    a.out = out; a.lse = lse; a.weights = attn_weights; a.status = dev_status;
+    a.q_stride = desc->q_stride ? desc->q_stride : (int64_t)desc->num_q_heads * desc->head_dim;
+    a.weight_stride = weight_stride(desc);
+    char* ws = static_cast<char*>(workspace);
+    a.cum = reinterpret_cast<int32_t*>(ws);
+    a.lse2 = reinterpret_cast<float*>(ws + y.lse2);
+    a.part_ml = reinterpret_cast<float2*>(ws + y.ml);
+    a.part_o = reinterpret_cast<float*>(ws + y.o);
+    a.scores = reinterpret_cast<float*>(ws + y.scores);
+    a.B = desc->batch; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = a.Hq / a.Hkv;
+    a.D = desc->head_dim; a.HT = y.plan.HT; a.GS = y.plan.GS; a.NG = y.plan.NG; a.grid = y.plan.grid;
+    a.max_len = cache_max_len(desc);
+    const float scale = desc->softmax_scale > 0.f ? desc->softmax_scale : 1.0f / sqrtf((float)desc->head_dim);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return tv::launch_decode(a, desc->dtype, y.plan, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TV_OK
+                                                                                                       : TV_ERR_CUDA;
+}
+
+tv_status tv_evict_cache(const tv_cache_desc* desc, int32_t budget, int32_t sink, int32_t recent, void* paged_k,
+                         void* paged_v, const int32_t* block_table, const int32_t* kv_lens, const float* weights,
+                         const int32_t* dst_block_table, float* weights_out, int32_t* kept, int32_t* new_kv_lens,
+                         int32_t* dev_status, void* stream) {
+    tv_status s = check_cache_desc(desc);
+    if (s != TV_OK) return s;
+    if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget) return TV_ERR_INVALID_ARG;
+    if (!paged_k || !paged_v || !block_table || !kv_lens || !weights || !kept || !new_kv_lens)
+        return TV_ERR_INVALID_ARG;
+    // other CTAs still read a sequence's length while its new length is written
+    if (new_kv_lens == kv_lens || dst_block_table == block_table) return TV_ERR_INVALID_ARG;
+    if (misaligned(paged_k) || misaligned(paged_v)) return TV_ERR_INVALID_ARG;
+    const int32_t max_len = cache_max_len(desc);
+    if (max_len > tv::evict_max_len()) return TV_ERR_UNSUPPORTED;
+    if ((int64_t)desc->batch * desc->num_kv_heads * 16 > INT32_MAX) return TV_ERR_UNSUPPORTED;
+    tv::EvictArgs a = {};
+    a.k = paged_k; a.v = paged_v; a.c = cache_view(desc, block_table); a.dst_table = dst_block_table;
+    a.lens = kv_lens; a.weights = weights; a.weights_out = weights_out; a.kept = kept; a.new_lens = new_kv_lens;
+    a.status = dev_status;
+    a.weight_stride = weight_stride(desc);
+    a.B = desc->batch; a.Hkv = desc->num_kv_heads; a.row_bytes = desc->head_dim * (int)elem_size(desc->dtype);
+    a.budget = budget; a.sink = sink; a.recent = recent; a.max_len = max_len;
+    return tv::launch_evict(a, device_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+tv_status tv_rotary_write(const tv_cache_desc* desc, const tv_rotary_desc* rot, const void* q, const void* k,
+                          const void* v, const float* inv_freq, const int32_t* parent_idx, const int32_t* positions,
+                          const int32_t* position_base, const int32_t* prefix_lens, const int32_t* block_table,
+                          void* q_out, void* paged_k, void* paged_v, int32_t* dev_status, void* stream) {
+    tv_status s = check_cache_desc(desc);
+    if (s != TV_OK) return s;
+    if (!rot || !k || !v || !inv_freq || !prefix_lens || !block_table || !paged_k || !paged_v) return TV_ERR_INVALID_ARG;
+    if (!q != !q_out) return TV_ERR_INVALID_ARG;
+    if (rot->num_nodes < 1 || rot->num_axes < 1 || rot->rotary_dim < 1 || rot->rotary_dim > desc->head_dim)
+        return TV_ERR_INVALID_ARG;
+    if (rot->rotary_dim % 16 || rot->num_axes > 4) return TV_ERR_UNSUPPORTED;
+    if (rot->interleaved != 0 && rot->interleaved != 1) return TV_ERR_INVALID_ARG;
+    if (parent_idx && !positions && rot->num_nodes > 1024) return TV_ERR_UNSUPPORTED;
+    if ((int64_t)desc->batch * rot->num_nodes > INT32_MAX) return TV_ERR_UNSUPPORTED;
+    for (int i = 0; i < rot->rotary_dim / 2; ++i)
+        if (rot->axis_of_pair[i] >= rot->num_axes) return TV_ERR_INVALID_ARG;
+    const int64_t qrow = (int64_t)desc->num_q_heads * desc->head_dim, krow = (int64_t)desc->num_kv_heads * desc->head_dim;
+    const int64_t qs = rot->q_stride ? rot->q_stride : qrow, ks = rot->k_stride ? rot->k_stride : krow,
+                  vs = rot->v_stride ? rot->v_stride : krow;
+    const int64_t es = (int64_t)elem_size(desc->dtype);
+    if (qs < qrow || ks < krow || vs < krow || qs * es % 16 || ks * es % 16 || vs * es % 16) return TV_ERR_INVALID_ARG;
+    if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_out) || misaligned(paged_k) ||
+        misaligned(paged_v))
+        return TV_ERR_INVALID_ARG;
+    if (q && q == q_out && qs != qrow) return TV_ERR_INVALID_ARG;
+    tv::RotaryArgs a = {};
+    a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.cache_k = paged_k; a.cache_v = paged_v;
+    a.c = cache_view(desc, block_table);
+    a.inv_freq = inv_freq; a.prefix_lens = prefix_lens; a.position_base = position_base; a.positions = positions;
+    a.parent = positions ? nullptr : parent_idx; a.counts = rot->node_counts; a.status = dev_status;
+    a.q_stride = qs; a.k_stride = ks; a.v_stride = vs;
+    a.B = desc->batch; a.N = rot->num_nodes; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads;
+    a.D = desc->head_dim; a.rot = rot->rotary_dim; a.interleaved = rot->interleaved; a.axes = rot->num_axes;
+    for (int i = 0; i < rot->rotary_dim / 2; ++i) a.axis_of_pair[i] = rot->axis_of_pair[i];
+    return tv::launch_rotary(a, desc->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
 }  // extern "C"

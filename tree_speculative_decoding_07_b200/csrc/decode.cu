@@ -1,0 +1,779 @@
+// decode.cu -- tv_decode_attention: one new token of every sequence attends to
+// its paged cache.
+//
+//   s_t = scale q . k_t,   out = sum_t exp(s_t - lse) v_t,   lse = log sum_t exp(s_t)
+//
+// and, when asked for, weights[b][h][t] += sum over the KV head's query heads
+// of exp(s_t - lse).
+//
+// Split.  The whole batch's work is one line of 16-token tiles, sequence by
+// sequence and KV head by KV head; every CTA takes an equal stretch of it,
+// whatever the sequences' lengths.  A stretch covers some heads whole (their
+// result is final) and at most two in part: those leave their running maximum,
+// sum and unnormalised output in the workspace, and a second kernel joins
+// them in stretch order (so the result does not depend on timing).
+//
+// Inside a CTA the four warps take tiles in turn.  Each warp keeps its own ring
+// of tiles (cp.async, three deep) and its own running softmax, so there is no
+// block barrier in the loop.
+//
+// bf16 and fp16 use warp-level matrix instructions (m16n8k16): S^T = K Q^T with
+// the tokens as rows and up to 8 query heads as columns, then O^T += V^T P^T; the
+// transposed 8x8 blocks of P come from movmatrix.  P goes into the product as a
+// high and a low 16-bit part, so no precision is lost to its rounding: the bytes
+// of K and V bound this kernel, not the matrix units.  fp32 runs on the CUDA
+// cores (two lanes per token for the scores, lanes over the head's dimensions
+// for the values).
+#include "kernels.h"
+#include "tv_common.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int TILE = 16;              // tokens per step of a warp
+constexpr int STAGES = 3;             // ring depth of a warp, in tiles
+constexpr int MIN_TILES = 8;          // a CTA's shortest stretch
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float BAD_SUM = -1.f;       // sum of a piece whose block table is out of range
+
+template <typename T, int D> struct Shape {
+    // Rows are padded so that the eight rows of one ldmatrix (16-bit types), or the
+    // four tokens times two halves of one 8-lane phase (fp32), fall into different banks.
+    static constexpr int ROW = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 32);
+    static constexpr int CH = D * (int)sizeof(T) / 16;  // 16-byte pieces of a row
+    static constexpr int STAGE = 2 * TILE * ROW;        // a tile of K and of V
+    static constexpr int RING = STAGES * STAGE;         // one warp's ring
+    // Warps per CTA: four rings fit the 227 KB of a CTA, but for fp32 rows of 1 KB.
+    static constexpr int NW = RING * 4 <= 224 * 1024 ? 4 : 2;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <typename T> struct Mma;
+template <> struct Mma<__nv_bfloat16> {
+    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    // two values as a pair of high parts and a pair of what those leave
+    static __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+};
+template <> struct Mma<__half> {
+    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+};
+
+// Tiles of sequence b (0 for a length out of range, which is reported elsewhere).
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
+    const int L = a.lens[b];
+    return L < 0 || L > a.max_len ? 0 : (L + TILE - 1) / TILE;
+}
+
+// The CTA's stretch [pos, end) of the line and where it starts.
+struct Start {
+    int total;   // tiles of the whole line
+    int b, cum;  // sequence that holds pos, and the tiles (per unit) before it
+};
+
+// Block-wide: thread i sums a run of sequences, the runs are scanned, and the
+// thread whose run holds `pos` walks it.
+template <int NW, typename F>
+__device__ __forceinline__ void find_start(const DecodeArgs& a, int units, F pos_of, bool write_cum, Start* s_start,
+                                           int* s_scan) {
+    constexpr int DE_THREADS = NW * 32;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int run = (a.B + DE_THREADS - 1) / DE_THREADS;
+    const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles_of(a, b);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    int before = inc - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += s_scan[w];
+        all += s_scan[w];
+    }
+    const int total = all * units;
+    const int pos = pos_of(total);
+    if (write_cum) {
+        int c = before;
+        for (int b = b0; b < b1; ++b) {
+            a.cum[b] = c;
+            c += tiles_of(a, b);
+        }
+        if (tid == 0) a.cum[a.B] = all;
+    }
+    if (tid == 0) s_start->total = total;
+    if (pos < total && pos >= before * units && pos < (before + sum) * units) {
+        int b = b0, c = before;
+        for (;; ++b) {
+            const int t = tiles_of(a, b);
+            if (pos < (c + t) * units) break;
+            c += t;
+        }
+        s_start->b = b;
+        s_start->cum = c;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int stretch(int total, int grid) {
+    const int per = (total + grid - 1) / grid;
+    return per < MIN_TILES ? MIN_TILES : per;
+}
+
+template <typename T, int D, int HT>
+__global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using S = Shape<T, D>;
+    constexpr int NW = S::NW, DE_THREADS = NW * 32;
+    constexpr bool MMA = sizeof(T) == 2;
+    constexpr int NT = MMA ? HT / 8 : 1;
+    constexpr int KS = D / 16;
+    constexpr int DV = D / 32;  // values per lane on the fp32 path
+    extern __shared__ __align__(16) unsigned char ring_all[];
+    __shared__ Start s_start;
+    __shared__ int s_scan[NW];
+    __shared__ float s_m[NW][HT], s_l[NW][HT];
+    __shared__ __align__(16) float s_q[MMA ? 1 : HT * D];
+    __shared__ __align__(16) float s_p[MMA ? 1 : NW][MMA ? 1 : TILE * HT];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int units = a.Hkv * a.NG;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // sequences without a token, and those whose length is out of range
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const int L = a.lens[b];
+        if (L > 0 && L <= a.max_len) continue;
+        if (L != 0 && tid == 0) report(a.status, TV_ERR_INVALID_ARG);
+        T* out = static_cast<T*>(a.out) + (size_t)b * a.Hq * D;
+        const float fill = L == 0 ? 0.f : __int_as_float(0x7fc00000);
+        for (int i = tid; i < a.Hq * D; i += DE_THREADS) Elem<T>::store(out + i, fill);
+        if (a.lse)
+            for (int i = tid; i < a.Hq; i += DE_THREADS)
+                a.lse[(size_t)b * a.Hq + i] = L == 0 ? -__int_as_float(0x7f800000) : fill;
+    }
+    find_start<NW>(a, units, [&](int total) { return (int)min((int64_t)total, (int64_t)blockIdx.x * stretch(total, a.grid)); },
+               blockIdx.x == 0, &s_start, s_scan);
+    const int total = s_start.total, per = stretch(total, a.grid);
+    const int64_t begin64 = (int64_t)blockIdx.x * per;
+    if (begin64 >= total) return;
+    const int begin = (int)begin64, end = (int)min((int64_t)total, begin64 + per);
+    int pos = begin, b = s_start.b, cum = s_start.cum;
+    int T_b = tiles_of(a, b);
+    int u = (pos - cum * units) / T_b, t0 = (pos - cum * units) - u * T_b;
+
+    unsigned char* ring = ring_all + warp * S::RING;
+    const uint32_t ring_a = smem_u32(ring);
+
+    while (pos < end) {
+        const int n = min(T_b - t0, end - pos);  // tiles of this piece
+        const int L = a.lens[b];
+        const int h = u / a.NG, g0 = (u - h * a.NG) * HT;
+        const int heads = min(HT, a.G - g0);     // query heads of this unit
+        const int32_t* table = a.c.table + (size_t)b * a.c.max_blocks;
+        const T* q = static_cast<const T*>(a.q) + (size_t)b * a.q_stride + (size_t)(h * a.G + g0) * D;
+        const char* kb = static_cast<const char*>(a.k) + (int64_t)h * a.c.head_stride;
+        const char* vb = static_cast<const char*>(a.v) + (int64_t)h * a.c.head_stride;
+
+        // the ring: tile i of the piece, for this warp i = warp, warp + NW, ...
+        int bad = 0;
+        auto offset_of = [&](int i) -> int64_t {  // lane's row of tile i, or -1
+            const int t = (t0 + i) * TILE + lane % TILE;
+            if (i >= n || t >= L) return -1;
+            const int blk = t / a.c.block_size;
+            const int id = table[blk];
+            if (id < 0 || id >= a.c.num_blocks) {
+                bad = 1;
+                return -1;
+            }
+            return (int64_t)id * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
+        };
+        auto issue = [&](int slot, int64_t off) {
+            const uint32_t dst = ring_a + slot * S::STAGE;
+            static_assert(TILE * S::CH % 32 == 0, "a tile is whole warps of pieces");
+#pragma unroll
+            for (int j = 0; j < TILE * S::CH / 32; ++j) {
+                const int x = j * 32 + lane, row = x / S::CH, ch = x - row * S::CH;
+                const int64_t o = __shfl_sync(0xffffffffu, off, row);
+                const int bytes = o < 0 ? 0 : 16;  // rows past the sequence are zeros
+                const int64_t at = (o < 0 ? 0 : o) + ch * 16;
+                cp_async16(dst + row * S::ROW + ch * 16, kb + at, bytes);
+                cp_async16(dst + TILE * S::ROW + row * S::ROW + ch * 16, vb + at, bytes);
+            }
+        };
+        int nxt = warp;  // next tile to request
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) {
+            if (nxt < n) issue(s, offset_of(nxt));
+            cp_commit();
+            nxt += NW;
+        }
+        int64_t off_next = offset_of(nxt);
+
+        // queries
+        uint32_t qf[MMA ? NT : 1][MMA ? KS : 1][2];
+        if constexpr (MMA) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int hd = j * 8 + lane / 4;
+                const T* row = q + (size_t)hd * D + (lane % 4) * 2;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    qf[j][kk][0] = hd < heads ? *reinterpret_cast<const uint32_t*>(row + kk * 16) : 0u;
+                    qf[j][kk][1] = hd < heads ? *reinterpret_cast<const uint32_t*>(row + kk * 16 + 8) : 0u;
+                }
+            }
+        } else {
+            __syncthreads();
+            for (int i = tid; i < HT * D; i += DE_THREADS) s_q[i] = i < heads * D ? reinterpret_cast<const float*>(q)[i] : 0.f;
+            __syncthreads();
+        }
+
+        // running softmax: a lane of the matrix path has two heads per 8 (columns
+        // 2 (lane % 4) and the next); on the fp32 path every lane has all HT
+        constexpr int NM = MMA ? 2 * NT : HT;
+        float m[NM], l[NM];
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+        float o[MMA ? NT * KS : HT][MMA ? 4 : DV];
+#pragma unroll
+        for (int i = 0; i < (MMA ? NT * KS : HT); ++i)
+#pragma unroll
+            for (int e = 0; e < (MMA ? 4 : DV); ++e) o[i][e] = 0.f;
+
+        int slot = 0;
+        for (int i = warp; i < n; i += NW) {
+            cp_wait<STAGES - 2>();
+            __syncwarp();
+            {  // the slot that the previous step read is free
+                int free_slot = slot + STAGES - 1;
+                if (free_slot >= STAGES) free_slot -= STAGES;
+                if (nxt < n) issue(free_slot, off_next);
+                cp_commit();
+                nxt += NW;
+                off_next = offset_of(nxt);
+            }
+            const uint32_t kt = ring_a + slot * S::STAGE, vt = kt + TILE * S::ROW;
+            const int tok = (t0 + i) * TILE;
+            float* sc = a.weights ? a.scores + ((size_t)(pos + i) * TILE) * a.GS : nullptr;
+            if constexpr (MMA) {
+                float c[NT][4];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    uint32_t f[4];
+                    ldsm4(f, kt + (lane % 16) * S::ROW + (kk * 2 + lane / 16) * 16);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) Mma<T>::run(c[j], f, qf[j][kk][0], qf[j][kk][1]);
+                }
+                const int r0 = lane / 4;
+                const bool in0 = tok + r0 < L, in1 = tok + r0 + 8 < L;
+                uint32_t ph[NT][2], pl[NT][2];
+                float corr[NM];
+                bool grew = false;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int hd = j * 8 + (lane % 4) * 2 + e;
+                        c[j][e] = in0 ? c[j][e] * a.scale_log2 : -INFINITY;
+                        c[j][2 + e] = in1 ? c[j][2 + e] * a.scale_log2 : -INFINITY;
+                        if (sc && hd < heads) {
+                            if (in0) sc[r0 * a.GS + hd] = c[j][e];
+                            if (in1) sc[(r0 + 8) * a.GS + hd] = c[j][2 + e];
+                        }
+                        float x = fmaxf(c[j][e], c[j][2 + e]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        const int k = 2 * j + e;
+                        const float mn = fmaxf(m[k], x);
+                        const float mu = mn == -INFINITY ? 0.f : mn;
+                        corr[k] = ex2(m[k] - mu);
+                        grew |= mn != m[k];
+                        m[k] = mn;
+                        c[j][e] = ex2(c[j][e] - mu);
+                        c[j][2 + e] = ex2(c[j][2 + e] - mu);
+                        l[k] = l[k] * corr[k] + (c[j][e] + c[j][2 + e]);
+                    }
+                    Mma<T>::split(c[j][0], c[j][1], ph[j][0], pl[j][0]);
+                    Mma<T>::split(c[j][2], c[j][3], ph[j][1], pl[j][1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        ph[j][e] = movm(ph[j][e]);
+                        pl[j][e] = movm(pl[j][e]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int x = 0; x < NT * KS; ++x) {
+                        const int j = x / KS;
+                        o[x][0] *= corr[2 * j];
+                        o[x][1] *= corr[2 * j + 1];
+                        o[x][2] *= corr[2 * j];
+                        o[x][3] *= corr[2 * j + 1];
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
+                    uint32_t f[4];
+                    ldsm4t(f, vt + ((lane % 8) + (lane / 16) * 8) * S::ROW + (d * 2 + (lane / 8) % 2) * 16);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        Mma<T>::run(o[j * KS + d], f, ph[j][0], ph[j][1]);
+                        Mma<T>::run(o[j * KS + d], f, pl[j][0], pl[j][1]);
+                    }
+                }
+            } else {
+                const unsigned char* kr = ring + slot * S::STAGE;
+                const unsigned char* vr = kr + TILE * S::ROW;
+                const int tk = lane / 2, half = lane % 2;
+                float acc[HT];
+#pragma unroll
+                for (int g = 0; g < HT; ++g) acc[g] = 0.f;
+#pragma unroll 4
+                for (int x = 0; x < D / 8; ++x) {
+                    const float4 kv = *reinterpret_cast<const float4*>(kr + tk * S::ROW + (2 * x + half) * 16);
+#pragma unroll
+                    for (int g = 0; g < HT; ++g) {
+                        const float4 qv = *reinterpret_cast<const float4*>(&s_q[g * D + (2 * x + half) * 4]);
+                        acc[g] = fmaf(kv.x, qv.x, acc[g]);
+                        acc[g] = fmaf(kv.y, qv.y, acc[g]);
+                        acc[g] = fmaf(kv.z, qv.z, acc[g]);
+                        acc[g] = fmaf(kv.w, qv.w, acc[g]);
+                    }
+                }
+                const bool in = tok + tk < L;
+                bool grew = false;
+                float corr[HT];
+#pragma unroll
+                for (int g = 0; g < HT; ++g) {
+                    float x = acc[g] + __shfl_xor_sync(0xffffffffu, acc[g], 1);
+                    x = in ? x * a.scale_log2 : -INFINITY;
+                    if (sc && half == 0 && in && g < heads) sc[tk * a.GS + g] = x;
+                    float y = x;
+#pragma unroll
+                    for (int d = 2; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                    const float mn = fmaxf(m[g], y);
+                    const float mu = mn == -INFINITY ? 0.f : mn;
+                    corr[g] = ex2(m[g] - mu);
+                    grew |= mn != m[g];
+                    m[g] = mn;
+                    const float p = ex2(x - mu);
+                    l[g] = l[g] * corr[g] + (half ? 0.f : p);
+                    if (half == 0) s_p[warp][tk * HT + g] = p;
+                }
+                __syncwarp();
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int g = 0; g < HT; ++g)
+#pragma unroll
+                        for (int e = 0; e < DV; ++e) o[g][e] *= corr[g];
+                }
+#pragma unroll 4
+                for (int t = 0; t < TILE; ++t) {
+                    float vv[DV];
+#pragma unroll
+                    for (int e = 0; e < DV; ++e) vv[e] = reinterpret_cast<const float*>(vr + t * S::ROW)[lane + 32 * e];
+#pragma unroll
+                    for (int g = 0; g < HT; ++g) {
+                        const float p = s_p[warp][t * HT + g];
+#pragma unroll
+                        for (int e = 0; e < DV; ++e) o[g][e] = fmaf(p, vv[e], o[g][e]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (++slot == STAGES) slot = 0;
+        }
+        cp_wait<0>();
+        __syncwarp();
+
+        // the warps' parts: common maximum, then sums (in warp order) through the rings
+#pragma unroll
+        for (int k = 0; k < NM; ++k) {
+#pragma unroll
+            for (int d = MMA ? 4 : 1; d < 32; d <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
+            const int hd = MMA ? (k / 2) * 8 + (lane % 4) * 2 + k % 2 : k;
+            if (MMA ? lane < 4 : lane == 0) {
+                s_m[warp][hd] = m[k];
+                s_l[warp][hd] = l[k];
+            }
+        }
+        const bool any_bad = __syncthreads_or(bad) != 0;
+        constexpr int OROW = D + 4;
+        static_assert(HT * OROW * 4 <= S::RING, "a warp's outputs fit its ring");
+        float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int k = 0; k < NM; ++k) {
+            const int hd = MMA ? (k / 2) * 8 + (lane % 4) * 2 + k % 2 : k;
+            float M = s_m[0][hd];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][hd]);
+            const float f = ex2(m[k] - (M == -INFINITY ? 0.f : M));
+            if constexpr (MMA) {
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
+                    so[hd * OROW + d * 16 + lane / 4] = o[(k / 2) * KS + d][k % 2] * f;
+                    so[hd * OROW + d * 16 + lane / 4 + 8] = o[(k / 2) * KS + d][2 + k % 2] * f;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < DV; ++e) so[hd * OROW + lane + 32 * e] = o[k][e] * f;
+            }
+        }
+        __syncthreads();
+        const bool whole = n == T_b;
+        const int part = 2 * blockIdx.x + (pos == begin ? 0 : 1);
+        if (any_bad && tid == 0) report(a.status, TV_ERR_BLOCK_TABLE);
+        for (int x = tid; x < heads * (D / 4); x += DE_THREADS) {
+            const int hd = x / (D / 4), d = (x - hd * (D / 4)) * 4;
+            float M = s_m[0][hd], sum = 0.f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][hd]);
+            const float mu = M == -INFINITY ? 0.f : M;
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                sum += s_l[w][hd] * ex2(s_m[w][hd] - mu);
+                const float4 y = *reinterpret_cast<const float4*>(ring_all + w * S::RING + (hd * OROW + d) * 4);
+                r.x += y.x;
+                r.y += y.y;
+                r.z += y.z;
+                r.w += y.w;
+            }
+            if (whole) {
+                float inv = sum == 0.f ? 0.f : 1.f / sum;
+                if (any_bad) inv = __int_as_float(0x7fc00000);
+                T* out = static_cast<T*>(a.out) + ((size_t)b * a.Hq + h * a.G + g0 + hd) * D + d;
+                Elem<T>::store(out, r.x * inv);
+                Elem<T>::store(out + 1, r.y * inv);
+                Elem<T>::store(out + 2, r.z * inv);
+                Elem<T>::store(out + 3, r.w * inv);
+                if (d == 0) {
+                    const size_t at = (size_t)b * a.Hq + h * a.G + g0 + hd;
+                    const float l2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+                    if (a.lse) a.lse[at] = any_bad ? __int_as_float(0x7fc00000) : l2 * LN2;
+                    // +inf marks a head whose weights stay as they were
+                    if (a.weights) a.lse2[at] = any_bad ? INFINITY : l2;
+                }
+            } else {
+                *reinterpret_cast<float4*>(a.part_o + ((size_t)part * HT + hd) * D + d) = r;
+                if (d == 0) a.part_ml[(size_t)part * HT + hd] = make_float2(M, any_bad ? BAD_SUM : sum);
+            }
+        }
+        __syncthreads();  // the rings and the shared values are free for the next piece
+
+        pos += n;
+        t0 = 0;
+        if (++u == units) {
+            u = 0;
+            cum += T_b;
+            if (pos < end) do T_b = tiles_of(a, ++b); while (T_b == 0);
+        }
+    }
+}
+
+// Where a unit's tiles lie on the line and which stretches cover them.
+struct Pieces {
+    int c0, c1, per, first;  // stretches c0 .. c1; first: the unit's first tile
+    __device__ __forceinline__ int slot(int c) const { return 2 * c + (c == c0 && c * per != first ? 1 : 0); }
+};
+__device__ __forceinline__ Pieces pieces_of(int first, int tiles, int per) {
+    Pieces p;
+    p.first = first;
+    p.per = per;
+    p.c0 = first / per;
+    p.c1 = (first + tiles - 1) / per;
+    return p;
+}
+
+// The sequence that holds tile-per-unit `x` of the cumulative counts (the last b with cum[b] <= x).
+__device__ __forceinline__ int find_seq(const int32_t* cum, int B, int64_t pos, int units) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((int64_t)cum[mid] * units <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+constexpr int JO_THREADS = 128;
+
+// Joins the pieces of the heads that several CTAs share, and adds the
+// weights.  Blocks 0 .. grid-1 (times the unit's query heads): block c joins the unit in
+// which stretch c begins, if stretch c is that unit's second.  The blocks after
+// them share the line of (sequence, KV head, tile) for the weights.
+template <typename T, int D, int HT>
+__global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_constant__ DecodeArgs a, int wblocks) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int units = a.Hkv * a.NG;
+    __shared__ float s_red[2][JO_THREADS / 32];
+    __shared__ float4 s_o[JO_THREADS];
+    __shared__ float s_lse[128];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int all = a.cum[a.B], total = all * units;
+    if (total == 0) return;
+    const int per = stretch(total, a.grid);
+    const int joins = a.grid * a.GS;
+    if ((int)blockIdx.x < joins) {
+        const int c = blockIdx.x / a.GS, hd = blockIdx.x - c * a.GS;
+        const int64_t pos = (int64_t)c * per;
+        if (c == 0 || pos >= total) return;
+        const int b = find_seq(a.cum, a.B, pos, units);
+        const int T_b = a.cum[b + 1] - a.cum[b], base = a.cum[b] * units;
+        const int u = ((int)pos - base) / T_b, first = base + u * T_b;
+        if (pos == first || pos - per > first) return;  // the unit's first stretch, or a later one than its second
+        const int h = u / a.NG, g0 = (u - h * a.NG) * HT;
+        if (g0 + hd >= a.G) return;
+        const Pieces p = pieces_of(first, T_b, per);
+        // maximum and sum over the pieces
+        float M = -INFINITY, bad = 0.f;
+        for (int i = p.c0 + tid; i <= p.c1; i += JO_THREADS) {
+            const float2 ml = a.part_ml[(size_t)p.slot(i) * HT + hd];
+            M = fmaxf(M, ml.x);
+            if (ml.y == BAD_SUM) bad = 1.f;
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, d));
+        }
+        if (lane == 0) {
+            s_red[0][warp] = M;
+            s_red[1][warp] = bad;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < JO_THREADS / 32; ++w) {
+            M = fmaxf(M, s_red[0][w]);
+            bad = fmaxf(bad, s_red[1][w]);
+        }
+        const float mu = M == -INFINITY ? 0.f : M;
+        constexpr int Q = D / 4, GR = JO_THREADS / Q;  // lanes of a row, rows at once
+        const int gr = tid / Q, d = tid - gr * Q;
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        if (gr < GR)
+            for (int i = p.c0 + gr; i <= p.c1; i += GR) {
+                const size_t at = (size_t)p.slot(i) * HT + hd;
+                const float2 ml = a.part_ml[at];
+                const float4 y = *reinterpret_cast<const float4*>(a.part_o + at * D + d * 4);
+                const float f = ex2(ml.x - mu);
+                sum += ml.y * f;
+                r.x += y.x * f;
+                r.y += y.y * f;
+                r.z += y.z * f;
+                r.w += y.w * f;
+            }
+        __shared__ float s_sum[JO_THREADS];
+        s_o[tid] = r;
+        s_sum[tid] = sum;
+        __syncthreads();
+        if (gr == 0) {
+#pragma unroll
+            for (int g = 1; g < GR; ++g) {
+                const float4 y = s_o[g * Q + d];
+                r.x += y.x;
+                r.y += y.y;
+                r.z += y.z;
+                r.w += y.w;
+                sum += s_sum[g * Q + d];
+            }
+            float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (bad != 0.f) inv = __int_as_float(0x7fc00000);
+            const size_t at = (size_t)b * a.Hq + h * a.G + g0 + hd;
+            T* out = static_cast<T*>(a.out) + at * D + d * 4;
+            Elem<T>::store(out, r.x * inv);
+            Elem<T>::store(out + 1, r.y * inv);
+            Elem<T>::store(out + 2, r.z * inv);
+            Elem<T>::store(out + 3, r.w * inv);
+            if (d == 0 && a.lse)
+                a.lse[at] = bad != 0.f ? __int_as_float(0x7fc00000) : sum == 0.f ? -INFINITY : (M + log2f(sum)) * LN2;
+        }
+        return;
+    }
+    // weights: an equal stretch of (sequence, KV head, tile) for every block
+    const int wb = blockIdx.x - joins;
+    const int64_t wtotal = (int64_t)all * a.Hkv;
+    const int64_t wper = (wtotal + wblocks - 1) / wblocks;
+    int64_t pos = wb * wper;
+    const int64_t end = min(wtotal, pos + wper);
+    if (pos >= end) return;
+    int b = find_seq(a.cum, a.B, pos, a.Hkv);
+    while (pos < end) {
+        const int T_b = a.cum[b + 1] - a.cum[b];
+        const int64_t base = (int64_t)a.cum[b] * a.Hkv;
+        const int h = (int)((pos - base) / T_b), t0 = (int)(pos - base - (int64_t)h * T_b);
+        const int n = (int)min((int64_t)(T_b - t0), end - pos);
+        // log-sum-exp of the KV head's query heads, a warp each
+        __syncthreads();
+        for (int g = warp; g < a.G; g += JO_THREADS / 32) {
+            const int k = g / HT, hd = g - k * HT, first = a.cum[b] * units + (h * a.NG + k) * T_b;
+            const Pieces p = pieces_of(first, T_b, per);
+            float x;
+            if (p.c0 == p.c1) {
+                x = a.lse2[(size_t)b * a.Hq + h * a.G + g];
+            } else {
+                float M = -INFINITY, sum = 0.f, bad = 0.f;
+                for (int i = p.c0 + lane; i <= p.c1; i += 32) {
+                    const float2 ml = a.part_ml[(size_t)p.slot(i) * HT + hd];
+                    M = fmaxf(M, ml.x);
+                    if (ml.y == BAD_SUM) bad = 1.f;
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1) {
+                    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                    bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, d));
+                }
+                const float mu = M == -INFINITY ? 0.f : M;
+                for (int i = p.c0 + lane; i <= p.c1; i += 32) {
+                    const float2 ml = a.part_ml[(size_t)p.slot(i) * HT + hd];
+                    sum += ml.y * ex2(ml.x - mu);
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                x = bad != 0.f ? INFINITY : sum == 0.f ? -INFINITY : M + log2f(sum);
+            }
+            if (lane == 0) s_lse[g] = x;
+        }
+        __syncthreads();
+        const int L = a.lens[b];
+        float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
+        bool skip = false;
+        for (int g = 0; g < a.G; ++g) skip |= s_lse[g] == INFINITY;
+        if (!skip)
+            for (int x = tid; x < n * TILE; x += JO_THREADS) {
+                const int t = t0 * TILE + x;
+                if (t >= L) break;
+                float sum = 0.f;
+                for (int k = 0; k < a.NG; ++k) {
+                    const size_t tile = (size_t)a.cum[b] * units + (size_t)(h * a.NG + k) * T_b;
+                    const float* sc = a.scores + (tile * TILE + t) * a.GS;
+                    const int heads = min(HT, a.G - k * HT);
+                    for (int g = 0; g < heads; ++g) {
+                        const float lse = s_lse[k * HT + g];
+                        sum += lse == -INFINITY ? 0.f : ex2(sc[g] - lse);
+                    }
+                }
+                w[t] += sum;
+            }
+        pos += n;
+        while (pos < end && pos >= (int64_t)a.cum[b + 1] * a.Hkv) ++b;
+    }
+}
+
+template <typename T, int D, int HT>
+cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
+    auto kern = decode_kernel<T, D, HT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Shape<T, D>::NW * Shape<T, D>::RING);
+    if (e != cudaSuccess) return e;
+    kern<<<p.grid, Shape<T, D>::NW * 32, Shape<T, D>::NW * Shape<T, D>::RING, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || (p.grid == 1 && !a.weights)) return e;
+    const int wblocks = a.weights ? 4 * p.grid : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid * a.GS + wblocks);
+    cfg.blockDim = dim3(JO_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, HT>, a, wblocks);
+}
+
+template <typename T, int HT>
+cudaError_t by_dim(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
+    switch (a.D) {
+        case 64: return launch<T, 64, HT>(a, p, st);
+        case 96: return launch<T, 96, HT>(a, p, st);
+        case 128: return launch<T, 128, HT>(a, p, st);
+        default:
+            if constexpr (HT <= 8) return launch<T, 256, HT>(a, p, st);
+            return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, int sms, DecodePlan* p) {
+    const int es = dtype == TV_F32 ? 4 : 2;
+    if (dtype == TV_F32) p->HT = G <= 4 ? 4 : 8;
+    else p->HT = G <= 8 || D > 128 ? 8 : 16;
+    p->NG = (G + p->HT - 1) / p->HT;
+    p->GS = G < p->HT ? G : p->HT;
+    const int ring = STAGES * 2 * TILE * (D * es + (es == 2 ? 16 : 32));
+    p->smem = ring * (ring * 4 <= 224 * 1024 ? 4 : 2);
+    const int fixed = 4096 + (es == 4 ? p->HT * D * 4 + 4 * TILE * p->HT * 4 : 0);  // static and reserved shared memory
+    int per_sm = (228 * 1024) / (p->smem + fixed);
+    if (per_sm < 1) per_sm = 1;
+    if (per_sm > 4) per_sm = 4;
+    const int64_t tiles = (int64_t)B * Hkv * p->NG * ((max_len + TILE - 1) / TILE);
+    int64_t grid = (tiles + MIN_TILES - 1) / MIN_TILES;
+    if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
+    if (grid < 1) grid = 1;
+    p->grid = (int)grid;
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, int dtype, const DecodePlan& p, cudaStream_t st) {
+    if (dtype == TV_BF16) return p.HT == 8 ? by_dim<__nv_bfloat16, 8>(a, p, st) : by_dim<__nv_bfloat16, 16>(a, p, st);
+    if (dtype == TV_F16) return p.HT == 8 ? by_dim<__half, 8>(a, p, st) : by_dim<__half, 16>(a, p, st);
+    return p.HT == 4 ? by_dim<float, 4>(a, p, st) : by_dim<float, 8>(a, p, st);
+}
+
+}  // namespace tv

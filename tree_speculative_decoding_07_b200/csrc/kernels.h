@@ -119,4 +119,79 @@ struct SelectArgs {
 size_t select_smem_bytes(int max_cand, int budget);
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st);
 
+// A paged cache as the cache calls see it: strides in bytes.
+struct CacheView {
+    const int32_t* table;  // [B][max_blocks]
+    int max_blocks, num_blocks, block_size;
+    int64_t block_stride, token_stride, head_stride;
+};
+
+// One new token's attention over the paged cache.
+struct DecodeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    CacheView c;
+    const int32_t* lens;   // [B] cached tokens
+    void* out;             // [B][Hq][D]
+    float* lse;            // [B][Hq] natural-log log-sum-exp, or NULL
+    float* weights;        // [B][Hkv][weight_stride] attention weight sums, or NULL
+    int64_t q_stride, weight_stride;  // elements
+    int32_t* status;
+    // workspace
+    int32_t* cum;          // [B + 1] 16-token tiles of the sequences before b
+    float* lse2;           // [B][Hq] log2-domain log-sum-exp of heads that one CTA finished (with weights)
+    float2* part_ml;       // [2 * grid][HT] running maximum and sum of the pieces
+    float* part_o;         // [2 * grid][HT][D] their unnormalised outputs
+    float* scores;         // [tile][16][GS] scaled scores, log2 domain (with weights)
+    int B, Hq, Hkv, G, D, HT, GS, NG, max_len, grid;
+    float scale_log2;
+};
+struct DecodePlan {
+    int HT, NG, GS, grid, smem;  // query heads per unit, units per KV head, heads of a full unit
+};
+// dtype: 0 bf16, 1 fp32, 2 fp16
+void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, int sms, DecodePlan* p);
+cudaError_t launch_decode(const DecodeArgs& a, int dtype, const DecodePlan& p, cudaStream_t st);
+
+// Rotary positions: q and k rotated, k and v written into the cache.
+struct RotaryArgs {
+    const void* q;         // may be NULL (with q_out)
+    const void* k;
+    const void* v;
+    void* q_out;           // [B][N][Hq][D]
+    void* cache_k;
+    void* cache_v;
+    CacheView c;
+    const float* inv_freq;          // [rot / 2]
+    const int32_t* prefix_lens;     // [B]
+    const int32_t* position_base;   // [B] or NULL (= prefix_lens)
+    const int32_t* positions;       // [axes][B][N] or NULL (base + depth)
+    const int32_t* parent;          // [B][N] or NULL (chains)
+    const int32_t* counts;          // [B] or NULL
+    int32_t* status;
+    int64_t q_stride, k_stride, v_stride;  // elements between consecutive nodes
+    int B, N, Hq, Hkv, D, rot, interleaved, axes;
+    uint8_t axis_of_pair[128];
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st);
+
+// Eviction by accumulated attention weight.
+struct EvictArgs {
+    void* k;
+    void* v;
+    CacheView c;
+    const int32_t* dst_table;  // [B][max_blocks], NULL: in place
+    const int32_t* lens;
+    const float* weights;
+    float* weights_out;        // may be NULL, may be weights
+    int32_t* kept;             // [B][Hkv][budget]
+    int32_t* new_lens;
+    int32_t* status;
+    int64_t weight_stride;
+    int B, Hkv, row_bytes, budget, sink, recent, max_len;
+};
+int evict_max_len();
+cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st);
+
 }  // namespace tv
