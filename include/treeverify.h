@@ -611,7 +611,7 @@ TV_API tv_status tv_decode_attention(const tv_cache_desc *desc, const void *q, c
  * TV_ERR_INVALID_ARG or TV_ERR_BLOCK_TABLE in *dev_status.  Two launches, no
  * workspace.
  */
-#define TV_EVICT_MAX_LEN 819200
+#define TV_EVICT_MAX_LEN 786432
 
 TV_API tv_status tv_evict_cache(const tv_cache_desc *desc, int32_t budget, int32_t sink, int32_t recent,
                                 void *paged_k, void *paged_v, const int32_t *block_table,

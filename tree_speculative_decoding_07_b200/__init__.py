@@ -14,6 +14,7 @@ allocate outputs/workspace with torch and raise on a non-OK status.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libtreeverify.so")
 TV_OK, TV_ERR_INVALID_ARG, TV_ERR_UNSUPPORTED, TV_ERR_TREE = 0, 1, 2, 3
 TV_ERR_BLOCK_TABLE, TV_ERR_WORKSPACE, TV_ERR_CUDA, TV_ERR_TIMEOUT = 4, 5, 6, 7
 TV_BF16, TV_F32, TV_F16 = 0, 1, 2
-TV_EVICT_MAX_LEN = 819200
+TV_EVICT_MAX_LEN = 786432
 TV_STATIC_SCRATCH_BYTES = 2 << 20
 
 
@@ -527,40 +528,29 @@ def tv_rotary_write(desc, rot, q, k, v, inv_freq, parent_idx, positions, positio
                                      _stream(stream)))
 
 
-class _Launch:
-    """The device and stream of a call on the cache: every tensor has to lie on the first
-    one's GPU, which is made current; what is allocated belongs to the stream that the
-    kernels run on (`stream`, or the GPU's current one)."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, stream, first, *others):
-        import torch
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError("all tensors must be CUDA tensors")
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"all tensors must be on one GPU: {dev} and {t.device}")
-        self.guards = []
-        if torch.cuda.current_device() != dev.index:
-            self.guards.append(torch.cuda.device(dev))
-        if stream is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            elif stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            self.stream = stream.cuda_stream
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _on_gpu(stream, first, others):
+    """The GPU that every tensor has to lie on, the stream to run on as an address, and the
+    contexts to enter for it (None: the call's GPU and stream are the current ones).  What is
+    allocated inside them belongs to the stream that the kernels run on."""
+    import torch
+    at = first.get_device()
+    if at < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"all tensors must be on one GPU: {first.device} and {t.device}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(at)
+        return raw, None if torch.cuda.current_device() == at else torch.cuda.device(at)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=first.device)
+    elif stream.device != first.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)  # makes its GPU current too
 
 
 def _want(name, t, dtype, shape, optional=False):
@@ -585,6 +575,11 @@ def cache_desc(k_cache, v_cache, block_table, num_q_heads: int | None = None, so
     """Descriptor of a paged cache from tensors: caches [nb][block][Hkv][D] of any
     strides with contiguous head rows (equal for K and V), block_table [B][max_blocks]
     int32."""
+    return TvCacheDesc(*_cache_fields(k_cache, v_cache, block_table, num_q_heads, softmax_scale, max_kv_len))
+
+
+def _cache_fields(k_cache, v_cache, block_table, num_q_heads, softmax_scale, max_kv_len):
+    """The values of the descriptor's fields up to head_stride."""
     import torch
     if not _cache_types:
         _cache_types.update({torch.bfloat16: TV_BF16, torch.float32: TV_F32, torch.float16: TV_F16})
@@ -602,8 +597,8 @@ def cache_desc(k_cache, v_cache, block_table, num_q_heads: int | None = None, so
         if _row_strides("v_cache", v_cache) != strides:
             raise ValueError("k_cache and v_cache must have the same strides")
     b, mb = block_table.shape
-    return TvCacheDesc(b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
-                       int(max_kv_len), *strides, 0, 0)
+    return (b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
+            int(max_kv_len), *strides)
 
 
 def _row_strides(name, c):
@@ -621,44 +616,66 @@ def _row_strides(name, c):
     return strides
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_call(gpu, with_weights, *fields):
+    """Descriptor and workspace size of a decode call of these sizes on this GPU (current)."""
+    desc = TvCacheDesc(*fields)
+    plan = tv_decode_attention_plan(desc, with_weights)
+    return desc, ctypes.byref(desc), plan.workspace_bytes
+
+
 def decode_attention(q, k_cache, v_cache, block_table, kv_lens, softmax_scale: float = 0.0, attn_weights=None,
                      out=None, lse=None, workspace=None, max_kv_len: int = 0, dev_status=None, stream=None):
     """Run tv_decode_attention: one new token per sequence, q [B][Hq][D] (sequences may lie
     apart), over the paged cache; returns (out, lse [B][Hq] float32).  attn_weights
     [B][Hkv][width] float32, width at least max_kv_len (default: the block table's
     capacity), is added to in place."""
+    raw, ctx = _on_gpu(stream, q, (k_cache, v_cache, block_table, kv_lens, attn_weights, out, lse, workspace,
+                                   dev_status))
+    if ctx is not None:
+        with ctx:
+            return _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse,
+                           workspace, max_kv_len, dev_status)
+    return _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse, workspace,
+                   max_kv_len, dev_status)
+
+
+def _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse, workspace,
+            max_kv_len, dev_status):
     import torch
     if q.dim() != 3 or q.dtype != k_cache.dtype:
         raise TypeError("q must be [batch][heads][head_dim] of the caches' type")
     B, Hq, D = q.shape
-    desc = cache_desc(k_cache, v_cache, block_table, Hq, softmax_scale, max_kv_len)
-    if desc.batch != B or desc.head_dim != D:
+    fields = _cache_fields(k_cache, v_cache, block_table, Hq, softmax_scale, max_kv_len)
+    if fields[0] != B or fields[3] != D:
         raise ValueError("q, block_table and the caches disagree on batch or head_dim")
+    q_stride = weight_stride = 0
     if not q.is_contiguous():
         if (D > 1 and q.stride(2) != 1) or (Hq > 1 and q.stride(1) != D):
             raise ValueError("q: the heads of a sequence must be contiguous")
-        desc.q_stride = q.stride(0) if B > 1 else 0
+        q_stride = q.stride(0) if B > 1 else 0
     _want("kv_lens", kv_lens, torch.int32, (B,))
     if attn_weights is not None:
-        _want("attn_weights", attn_weights, torch.float32, (B, desc.num_kv_heads, attn_weights.shape[-1]))
-        desc.weight_stride = attn_weights.shape[2]
-    with _Launch(stream, q, k_cache, v_cache, block_table, kv_lens, attn_weights, out, lse, workspace,
-                 dev_status) as st:
-        if out is None:
-            out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-        else:
-            _want("out", out, q.dtype, (B, Hq, D))
-        if lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        else:
-            _want("lse", lse, torch.float32, (B, Hq))
-        if workspace is None:
-            ws_bytes = tv_decode_attention_workspace_size(desc, attn_weights is not None)
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        elif not workspace.is_contiguous():
+        weight_stride = attn_weights.shape[-1]
+        _want("attn_weights", attn_weights, torch.float32, (B, fields[2], weight_stride))
+    desc, ref, ws_bytes = _decode_call(q.get_device(), attn_weights is not None, *fields, q_stride, weight_stride)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _want("out", out, q.dtype, (B, Hq, D))
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _want("lse", lse, torch.float32, (B, Hq))
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    else:
+        if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        s = tv_decode_attention(desc, q, k_cache, v_cache, block_table, kv_lens, out, lse, attn_weights, workspace,
-                                workspace.numel() * workspace.element_size(), dev_status, st)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    s = lib().tv_decode_attention(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                  kv_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), _addr(attn_weights),
+                                  workspace.data_ptr(), ws_bytes, _addr(dev_status), raw)
     if s != TV_OK:
         raise TreeVerifyError(s, "tv_decode_attention")
     return out, lse
@@ -670,27 +687,38 @@ def evict_cache(k_cache, v_cache, block_table, kv_lens, weights, budget: int, si
     """Run tv_evict_cache on the caches (in place, or into the blocks of dst_block_table);
     returns (new_kv_lens [B], kept [B][Hkv][budget]), int32.  weights [B][Hkv][width]
     float32; weights_out, of its shape, may be weights itself."""
+    raw, ctx = _on_gpu(stream, k_cache, (v_cache, block_table, kv_lens, weights, dst_block_table, weights_out, kept,
+                                         new_kv_lens, dev_status))
+    if ctx is not None:
+        with ctx:
+            return _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table,
+                          weights_out, kept, new_kv_lens, max_kv_len, dev_status)
+    return _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table,
+                  weights_out, kept, new_kv_lens, max_kv_len, dev_status)
+
+
+def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table, weights_out,
+           kept, new_kv_lens, max_kv_len, dev_status):
     import torch
-    desc = cache_desc(k_cache, v_cache, block_table, None, 0.0, max_kv_len)
-    B, Hkv = desc.batch, desc.num_kv_heads
+    fields = _cache_fields(k_cache, v_cache, block_table, None, 0.0, max_kv_len)
+    B, Hkv, budget = fields[0], fields[2], int(budget)
     _want("kv_lens", kv_lens, torch.int32, (B,))
     _want("weights", weights, torch.float32, (B, Hkv, weights.shape[-1]))
     _want("weights_out", weights_out, torch.float32, weights.shape, optional=True)
     _want("dst_block_table", dst_block_table, torch.int32, block_table.shape, optional=True)
-    desc.weight_stride = weights.shape[2]
-    budget = int(budget)
-    with _Launch(stream, k_cache, v_cache, block_table, kv_lens, weights, dst_block_table, weights_out, kept,
-                 new_kv_lens, dev_status) as st:
-        if kept is None:
-            kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
-        else:
-            _want("kept", kept, torch.int32, (B, Hkv, budget))
-        if new_kv_lens is None:
-            new_kv_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
-        else:
-            _want("new_kv_lens", new_kv_lens, torch.int32, (B,))
-        s = tv_evict_cache(desc, budget, sink, recent, k_cache, v_cache, block_table, kv_lens, weights,
-                           dst_block_table, weights_out, kept, new_kv_lens, dev_status, st)
+    desc = TvCacheDesc(*fields, 0, weights.shape[-1])
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+    else:
+        _want("kept", kept, torch.int32, (B, Hkv, budget))
+    if new_kv_lens is None:
+        new_kv_lens = torch.empty_like(kv_lens)
+    else:
+        _want("new_kv_lens", new_kv_lens, torch.int32, (B,))
+    s = lib().tv_evict_cache(ctypes.byref(desc), budget, int(sink), int(recent), k_cache.data_ptr(),
+                             v_cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), weights.data_ptr(),
+                             _addr(dst_block_table), _addr(weights_out), kept.data_ptr(), new_kv_lens.data_ptr(),
+                             _addr(dev_status), raw)
     if s != TV_OK:
         raise TreeVerifyError(s, "tv_evict_cache")
     return new_kv_lens, kept
@@ -718,17 +746,30 @@ def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=N
     (position_base, else prefix_lens) plus the node's depth under parent_idx (None: chains);
     axis_of_pair: the axis of each frequency (a sequence of rotary_dim / 2 integers; None:
     axis 0)."""
+    raw, ctx = _on_gpu(stream, k, (v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx,
+                                   positions, position_base, node_counts, dev_status))
+    if ctx is not None:
+        with ctx:
+            return _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx,
+                           positions, position_base, axis_of_pair, interleaved, node_counts, dev_status)
+    return _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
+                   position_base, axis_of_pair, interleaved, node_counts, dev_status)
+
+
+def _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
+            position_base, axis_of_pair, interleaved, node_counts, dev_status):
     import torch
     if k.dim() != 4 or v.shape != k.shape or k.dtype != k_cache.dtype or v.dtype != k.dtype:
         raise TypeError("k and v must be [batch][nodes][num_kv_heads][head_dim] of the caches' type")
     B, N, Hkv, D = k.shape
-    Hq = Hkv
+    Hq, q_stride = Hkv, 0
     if q is not None:
         if q.dim() != 4 or q.dtype != k.dtype or q.shape[:2] != k.shape[:2] or q.shape[3] != D:
             raise TypeError("q must be [batch][nodes][num_q_heads][head_dim] of k's type")
         Hq = q.shape[2]
-    desc = cache_desc(k_cache, v_cache, block_table, Hq)
-    if (desc.batch, desc.num_kv_heads, desc.head_dim) != (B, Hkv, D):
+        q_stride = _node_stride("q", q)
+    fields = _cache_fields(k_cache, v_cache, block_table, Hq, 0.0, 0)
+    if fields[0] != B or fields[2] != Hkv or fields[3] != D:
         raise ValueError("k, block_table and the caches disagree on batch, heads or head_dim")
     pairs = inv_freq.numel()
     _want("inv_freq", inv_freq, torch.float32, (pairs,))
@@ -736,8 +777,8 @@ def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=N
     _want("position_base", position_base, torch.int32, (B,), optional=True)
     _want("parent_idx", parent_idx, torch.int32, (B, N), optional=True)
     _want("node_counts", node_counts, torch.int32, (B,), optional=True)
-    rot = TvRotaryDesc()
-    rot.num_nodes, rot.rotary_dim, rot.interleaved, rot.num_axes = N, 2 * pairs, int(bool(interleaved)), 1
+    rot = TvRotaryDesc(N, 2 * pairs, int(bool(interleaved)), 1, q_stride, _node_stride("k", k), _node_stride("v", v),
+                       _addr(node_counts))
     if axis_of_pair is not None:
         axes = bytes(axis_of_pair)
         if len(axes) != pairs or pairs > 128:
@@ -749,19 +790,14 @@ def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=N
         if positions.shape[0] < rot.num_axes:
             raise ValueError("axis_of_pair names an axis that positions lacks")
         rot.num_axes = positions.shape[0]
-    if node_counts is not None:
-        rot.node_counts = node_counts.data_ptr()
-    rot.k_stride, rot.v_stride = _node_stride("k", k), _node_stride("v", v)
-    if q is not None:
-        rot.q_stride = _node_stride("q", q)
-    with _Launch(stream, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
-                 position_base, node_counts, dev_status) as st:
-        if q is not None and q_out is None:
-            q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-        elif q_out is not None:
-            _want("q_out", q_out, k.dtype, (B, N, Hq, D))
-        s = tv_rotary_write(desc, rot, q, k, v, inv_freq, parent_idx, positions, position_base, prefix_lens,
-                            block_table, q_out, k_cache, v_cache, dev_status, st)
+    if q_out is not None:
+        _want("q_out", q_out, k.dtype, (B, N, Hq, D))
+    elif q is not None:
+        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+    s = lib().tv_rotary_write(ctypes.byref(TvCacheDesc(*fields, 0, 0)), ctypes.byref(rot), _addr(q), k.data_ptr(),
+                              v.data_ptr(), inv_freq.data_ptr(), _addr(parent_idx), _addr(positions),
+                              _addr(position_base), prefix_lens.data_ptr(), block_table.data_ptr(), _addr(q_out),
+                              k_cache.data_ptr(), v_cache.data_ptr(), _addr(dev_status), raw)
     if s != TV_OK:
         raise TreeVerifyError(s, "tv_rotary_write")
     return q_out

@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
 template <typename T, int D, int HT>
 cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
     auto kern = decode_kernel<T, D, HT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Shape<T, D>::NW * Shape<T, D>::RING);
+    static SmemLimit limit;  // one size for every call of this kernel
+    cudaError_t e = limit.allow((const void*)kern, Shape<T, D>::NW * Shape<T, D>::RING);
     if (e != cudaSuccess) return e;
     kern<<<p.grid, Shape<T, D>::NW * 32, Shape<T, D>::NW * Shape<T, D>::RING, st>>>(a);
     e = cudaGetLastError();

@@ -33,8 +33,9 @@ namespace {
 constexpr int SE_THREADS = 512;
 constexpr int SE_WARPS = SE_THREADS / 32;
 constexpr int SE_MAX_CLUSTER = 16;
-constexpr int SE_MAX_SLICE = 51200;  // sums in one CTA's shared memory (200 KB)
+constexpr int SE_MAX_SLICE = 49152;  // sums in one CTA's shared memory (192 KB)
 constexpr int BINS = 2048;
+constexpr int SE_UN = 4;             // sums a thread loads at once
 
 // Order-preserving key of a sum: larger sums, larger keys; NaN 0; -0 as +0.
 __device__ __forceinline__ uint32_t sum_key(float w) {
@@ -44,10 +45,11 @@ __device__ __forceinline__ uint32_t sum_key(float w) {
 }
 
 struct SelectShared {
-    uint32_t hist[3][BINS];
-    uint32_t scan[SE_WARPS + 1];
-    uint32_t wgt[SE_WARPS], weq[SE_WARPS];   // kept for certain / equal to the threshold, per warp
-    uint32_t cta_keep, cta_eq;               // the CTA's counts, read by its peers
+    uint32_t own[BINS];         // this CTA's counts of the current digit
+    uint32_t total[3][BINS];    // the cluster's, added up by its CTAs
+    uint32_t scan[SE_WARPS];
+    uint2 warp_cnt[SE_WARPS];   // kept for certain, equal to the threshold
+    uint2 cta_cnt;              // the CTA's sums of those, read by its peers
     uint32_t digit, above;
     int bad;
 };
@@ -59,6 +61,7 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int bh = blockIdx.x / C, b = bh / a.Hkv, h = bh - b * a.Hkv;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t L = a.lens[b];
     int32_t* kept = a.kept + (size_t)bh * a.budget;
     const bool lead = h == 0 && rank == 0 && tid == 0;
@@ -71,9 +74,33 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
         return;
     }
     const int n = L < a.budget ? L : a.budget;
+    const bool cut = L > a.budget;
+    const int want = cut ? a.budget - a.sink - a.recent : 0;
     if (tid == 0) s.bad = 0;
-    for (int i = tid; i < 3 * BINS; i += SE_THREADS) (&s.hist[0][0])[i] = 0;
+    if (want) {
+        for (int i = tid; i < BINS; i += SE_THREADS) s.own[i] = 0;
+        for (int i = tid; i < 3 * BINS; i += SE_THREADS) (&s.total[0][0])[i] = 0;
+    }
     __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the totals are cleared
+    // this CTA's slice of the sums
+    const int slice = (L + C - 1) / C;
+    const int t0 = min(L, rank * slice), t1 = min(L, t0 + slice);
+    const float* w = a.weights + (size_t)bh * a.weight_stride;
+    const int lo = min(a.sink, L), hi = max(lo, L - a.recent);  // candidates [lo, hi)
+    for (int t = t0 + tid; t < t1; t += SE_UN * SE_THREADS) {
+        float x[SE_UN];
+#pragma unroll
+        for (int i = 0; i < SE_UN; ++i) x[i] = t + i * SE_THREADS < t1 ? w[t + i * SE_THREADS] : 0.f;
+#pragma unroll
+        for (int i = 0; i < SE_UN; ++i) {
+            const int y = t + i * SE_THREADS;
+            if (y < t1) {
+                s_w[y - t0] = x[i];
+                if (want && y >= lo && y < hi) atomicAdd(&s.own[sum_key(x[i]) >> 21], 1u);
+            }
+        }
+    }
     // block ids of the span that is read and of the one that is written
     {
         const int32_t* bt = a.c.table + (size_t)b * a.c.max_blocks;
@@ -87,23 +114,10 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             bad |= dt[i] < 0 || dt[i] >= a.c.num_blocks;
         if (bad) s.bad = 1;
     }
-    // this CTA's slice of the sums
-    const int slice = (L + C - 1) / C;
-    const int t0 = min(L, rank * slice), t1 = min(L, t0 + slice);
-    const float* w = a.weights + (size_t)bh * a.weight_stride;
-    const int lo = min(a.sink, L), hi = max(lo, L - a.recent);  // candidates [lo, hi)
-    const bool cut = L > a.budget;
-    const int want = cut ? a.budget - a.sink - a.recent : 0;
-    for (int t = t0 + tid; t < t1; t += SE_THREADS) {
-        const float x = w[t];
-        s_w[t - t0] = x;
-        if (want && t >= lo && t < hi) atomicAdd(&s.hist[0][sum_key(x) >> 21], 1u);
-    }
-    cluster.sync();
-    int bad = 0;
-    for (int c = 0; c < C; ++c) bad |= *cluster.map_shared_rank(&s.bad, c);
+    __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     uint32_t prefix = 0, left = (uint32_t)want;  // key bits found so far; how many are still to be taken
-    if (want && !bad) {
+    if (want) {
         constexpr int PER = BINS / SE_THREADS;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
@@ -112,19 +126,26 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
                 const uint32_t mask = pass == 1 ? 2047u : 1023u;
                 for (int t = max(t0, lo) + tid; t < min(t1, hi); t += SE_THREADS) {
                     const uint32_t key = sum_key(s_w[t - t0]);
-                    if ((key ^ prefix) >> keep_shift == 0) atomicAdd(&s.hist[pass][(key >> shift) & mask], 1u);
+                    if ((key ^ prefix) >> keep_shift == 0) atomicAdd(&s.own[(key >> shift) & mask], 1u);
                 }
-                cluster.sync();
+                __syncthreads();
             }
-            // bins from the top down: thread i holds bins BINS - 1 - PER i and below
+            // every CTA adds its counts (few bins hold any) to each one's totals
             uint32_t cnt[PER], sum = 0;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) cnt[e] = 0;
-            for (int c = 0; c < C; ++c) {
-                const uint32_t* peer = cluster.map_shared_rank(&s.hist[pass][0], c);
-#pragma unroll
-                for (int e = 0; e < PER; ++e) cnt[e] += peer[BINS - 1 - (PER * tid + e)];
+            for (int e = 0; e < PER; ++e) {
+                const int bin = BINS - 1 - (PER * tid + e);
+                cnt[e] = s.own[bin];
+                if (C > 1 && cnt[e])
+                    for (int c = 0; c < C; ++c) atomicAdd(cluster.map_shared_rank(&s.total[pass][bin], c), cnt[e]);
+                s.own[bin] = 0;
             }
+            if (C > 1) {
+                cluster.sync();
+#pragma unroll
+                for (int e = 0; e < PER; ++e) cnt[e] = s.total[pass][BINS - 1 - (PER * tid + e)];
+            }
+            // bins from the top down: thread i holds bins BINS - 1 - PER i and below
 #pragma unroll
             for (int e = 0; e < PER; ++e) sum += cnt[e];
             uint32_t inc = sum;
@@ -135,8 +156,7 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             }
             if (lane == 31) s.scan[warp] = inc;
             __syncthreads();
-            uint32_t before = inc - sum;
-            for (int x = 0; x < warp; ++x) before += s.scan[x];
+            uint32_t before = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s.scan[lane] : 0u);
             if (before < left && left <= before + sum) {
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
@@ -150,155 +170,191 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             __syncthreads();
             prefix |= s.digit << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
             left -= s.above;
-            __syncthreads();
         }
     }
     // prefix is now the smallest kept key, left how many of its equals are kept
-    const bool select = cut && !bad;
-    auto sure = [&](int t, uint32_t key) {
-        return !cut || t < lo || t >= hi || (want && key > prefix);
+    auto classify = [&](int t, float x, bool& sure, bool& equal) {
+        const uint32_t key = sum_key(x);
+        sure = !cut || t < lo || t >= hi || (want && key > prefix);
+        equal = !sure && want && key == prefix;
     };
     const int per = ((t1 - t0 + SE_WARPS - 1) / SE_WARPS + 31) / 32 * 32;
     const int w0 = min(t1, t0 + warp * per), w1 = min(t1, w0 + per);
     uint32_t nk = 0, ne = 0;
-    for (int t = w0 + lane; t - lane < w1; t += 32) {
-        const bool in = t < w1;
-        const uint32_t key = in ? sum_key(s_w[t - t0]) : 0;
-        const bool k = in && sure(t, key);
-        const bool e = in && !k && select && want && key == prefix;
-        nk += __popc(__ballot_sync(0xffffffffu, k));
-        ne += __popc(__ballot_sync(0xffffffffu, e));
+    for (int t = w0 + lane; t < w1; t += 32) {
+        bool k, e;
+        classify(t, s_w[t - t0], k, e);
+        nk += k;
+        ne += e;
     }
-    if (lane == 0) {
-        s.wgt[warp] = nk;
-        s.weq[warp] = ne;
-    }
+    nk = __reduce_add_sync(0xffffffffu, nk);
+    ne = __reduce_add_sync(0xffffffffu, ne);
+    if (lane == 0) s.warp_cnt[warp] = make_uint2(nk, ne);
     __syncthreads();
-    if (tid == 0) {
-        uint32_t k = 0, e = 0;
-        for (int x = 0; x < SE_WARPS; ++x) {
-            k += s.wgt[x];
-            e += s.weq[x];
+    // before this warp: kept for certain, equals
+    const uint2 wc = lane < SE_WARPS ? s.warp_cnt[lane] : make_uint2(0, 0);
+    uint32_t bk = __reduce_add_sync(0xffffffffu, lane < warp ? wc.x : 0u);
+    uint32_t be = __reduce_add_sync(0xffffffffu, lane < warp ? wc.y : 0u);
+    int bad = s.bad;
+    if (C > 1) {
+        if (warp == 0) {
+            const uint32_t k = __reduce_add_sync(0xffffffffu, wc.x), e = __reduce_add_sync(0xffffffffu, wc.y);
+            if (lane == 0) s.cta_cnt = make_uint2(k, e);
         }
-        s.cta_keep = k;
-        s.cta_eq = e;
+        cluster.sync();  // every slice is in shared memory: the sums may be overwritten
+        uint2 pc = make_uint2(0, 0);
+        int pb = 0;
+        if (lane < C) {
+            pc = *cluster.map_shared_rank(&s.cta_cnt, lane);
+            pb = *cluster.map_shared_rank(&s.bad, lane);
+        }
+        bk += __reduce_add_sync(0xffffffffu, lane < rank ? pc.x : 0u);
+        be += __reduce_add_sync(0xffffffffu, lane < rank ? pc.y : 0u);
+        bad = __any_sync(0xffffffffu, pb);
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
-    cluster.sync();  // every slice is in shared memory: the sums may be overwritten
-    uint32_t bk = 0, be = 0;  // before this warp: kept for certain, equals
-    for (int c = 0; c < rank; ++c) {
-        bk += *cluster.map_shared_rank(&s.cta_keep, c);
-        be += *cluster.map_shared_rank(&s.cta_eq, c);
-    }
-    cluster.sync();  // no CTA leaves while a peer reads its counts
     if (bad) {
         if (lead) {
             a.new_lens[b] = L;
             report(a.status, TV_ERR_BLOCK_TABLE);
         }
         for (int r = rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
-        return;
-    }
-    for (int x = 0; x < warp; ++x) {
-        bk += s.wgt[x];
-        be += s.weq[x];
-    }
-    float* wo = a.weights_out ? a.weights_out + (size_t)bh * a.weight_stride : nullptr;
-    for (int t = w0 + lane; t - lane < w1; t += 32) {
-        const bool in = t < w1;
-        const float x = in ? s_w[t - t0] : 0.f;
-        const uint32_t key = in ? sum_key(x) : 0;
-        const bool k = in && sure(t, key);
-        const bool e = in && !k && select && want && key == prefix;
-        const uint32_t kb = __ballot_sync(0xffffffffu, k), eb = __ballot_sync(0xffffffffu, e);
+    } else {
+        float* wo = a.weights_out ? a.weights_out + (size_t)bh * a.weight_stride : nullptr;
         const uint32_t below = (1u << lane) - 1;
-        const uint32_t my_eq = be + __popc(eb & below);  // equals before this one
-        if (k || (e && my_eq < left)) {
-            const uint32_t r = bk + __popc(kb & below) + min(my_eq, left);
-            kept[r] = t;
-            if (wo) wo[r] = x;
+        for (int t = w0; t < w1; t += 32) {
+            const bool in = t + lane < w1;
+            const float x = in ? s_w[t + lane - t0] : 0.f;
+            bool k, e;
+            classify(t + lane, x, k, e);
+            const uint32_t kb = __ballot_sync(0xffffffffu, in && k), eb = __ballot_sync(0xffffffffu, in && e);
+            const uint32_t my_eq = be + __popc(eb & below);  // equals before this one
+            if (in && (k || (e && my_eq < left))) {
+                const uint32_t r = bk + __popc(kb & below) + min(my_eq, left);
+                kept[r] = t + lane;
+                if (wo) wo[r] = x;
+            }
+            bk += __popc(kb);
+            be += __popc(eb);
         }
-        bk += __popc(kb);
-        be += __popc(eb);
+        for (int r = n + rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
+        if (wo)
+            for (int t = max(t0, n) + tid; t < t1; t += SE_THREADS) wo[t] = 0.f;
+        if (lead) a.new_lens[b] = n;
     }
-    for (int r = n + rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
-    if (wo)
-        for (int t = max(t0, n) + tid; t < t1; t += SE_THREADS) wo[t] = 0.f;
-    if (lead) a.new_lens[b] = n;
+    __syncwarp();
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no peer reads this CTA's counts any more
 }
 
-constexpr int MV_THREADS = 256;
-constexpr int MV_UN = 8;                      // 16-byte pieces in flight per thread
-constexpr int MV_PIECES = MV_THREADS * MV_UN;  // pieces per CTA and chunk
+constexpr int MV_WARPS = 4;
+constexpr int MV_THREADS = MV_WARPS * 32;
+constexpr int MV_STAGE = 8192;  // bytes of a warp's step
+constexpr int MV_STAGES = 2;
 
-__global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_constant__ EvictArgs a, int rows_per_cta,
-                                                                int ctas) {
-    const bool in_place = a.dst_table == nullptr;
-    const int tid = threadIdx.x;
-    // in place: one cluster of `ctas` walks the head's rows; else `ctas` independent CTAs share them
-    const int bh = blockIdx.x / ctas, part = blockIdx.x - bh * ctas, b = bh / a.Hkv, h = bh - b * a.Hkv;
+__device__ __forceinline__ void mv_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
+// Work of `ctas` CTAs (a cluster in place): the K rows or the V rows of one (sequence, KV head).
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_constant__ EvictArgs a, int ctas) {
+    extern __shared__ __align__(16) uint4 mv_ring[];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int unit = blockIdx.x / ctas, part = blockIdx.x - unit * ctas, bh = unit / 2, b = bh / a.Hkv, h = bh - b * a.Hkv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t L = a.lens[b];
     if (L < 0 || L > a.max_len) return;
     const int n = L < a.budget ? L : a.budget;
-    if (in_place && n == L) return;  // nothing moves
+    if (IN_PLACE && n == L) return;  // nothing moves
     const int32_t* kept = a.kept + (size_t)bh * a.budget;
     if (n == 0 || kept[0] < 0) return;  // flagged by the selection
     const int32_t* bt = a.c.table + (size_t)b * a.c.max_blocks;
-    const int32_t* dt = in_place ? bt : a.dst_table + (size_t)b * a.c.max_blocks;
+    const int32_t* dt = IN_PLACE ? bt : a.dst_table + (size_t)b * a.c.max_blocks;
     const int cpr = a.row_bytes / 16;
-    const int64_t head = (int64_t)h * a.c.head_stride;
+    const int rows = min(32, MV_STAGE / a.row_bytes);  // rows of a warp's step, one lane's offsets each
+    char* base = static_cast<char*>(unit & 1 ? a.v : a.k) + (int64_t)h * a.c.head_stride;
     auto row_off = [&](const int32_t* tab, int t) {
         const int blk = t / a.c.block_size;
-        return (int64_t)tab[blk] * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride + head;
+        return (int64_t)tab[blk] * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
     };
-    const int chunk = rows_per_cta * ctas;
-    for (int r0 = 0; r0 < n; r0 += chunk) {
-        const int first = r0 + part * rows_per_cta;
-        uint4 buf[MV_UN];
-        int64_t to[MV_UN];
-#pragma unroll
-        for (int i = 0; i < MV_UN; ++i) {
-            const int x = i * MV_THREADS + tid;
-            const int row = x / (2 * cpr), y = x - row * 2 * cpr;  // y: piece of the K row, then of the V row
-            const int r = first + row;
-            to[i] = -1;
-            if (row < rows_per_cta && r < n) {
-                const int src = kept[r];
-                if (!in_place || src != r) {
-                    const bool isv = y >= cpr;
-                    const int64_t piece = (int64_t)(isv ? y - cpr : y) * 16;
-                    buf[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(isv ? a.v : a.k) +
-                                                             row_off(bt, src) + piece);
-                    to[i] = row_off(dt, r) + piece;
-                }
+    uint4* ring = mv_ring + warp * (MV_STAGES * MV_STAGE / 16);
+    const int chunk = rows * MV_WARPS * ctas, first = (part * MV_WARPS + warp) * rows;
+    const int pieces = rows * cpr, drow = 32 / cpr, dpiece = 32 - drow * cpr;
+    const int row0 = lane / cpr, piece0 = lane - row0 * cpr;
+    const int steps = (n + chunk - 1) / chunk;
+    // lane's row of step s: where it comes from and goes to (-1: nothing to move)
+    auto offsets = [&](int s, int64_t& src, int64_t& dst) {
+        src = dst = -1;
+        const int r = s * chunk + first + lane;
+        if (s >= steps || lane >= rows || r >= n) return;
+        const int t = kept[r];
+        if (IN_PLACE && t == r) return;
+        src = row_off(bt, t);
+        dst = row_off(dt, r);
+    };
+    auto load = [&](int stage, int64_t src) {
+        int row = row0, piece = piece0;
+        for (int x = lane; x - lane < pieces; x += 32) {
+            const int64_t o = __shfl_sync(0xffffffffu, src, row & 31);
+            if (x < pieces && o >= 0) mv_async16(ring + stage * (MV_STAGE / 16) + x, base + o + piece * 16);
+            row += drow;
+            piece += dpiece;
+            if (piece >= cpr) {
+                piece -= cpr;
+                ++row;
             }
         }
-        if (in_place) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int64_t src, dst, src_next, dst_next, dst_cur;
+    offsets(0, src, dst_cur);
+    load(0, src);
+    offsets(1, src_next, dst_next);
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) load((s + 1) % MV_STAGES, src_next);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        dst = dst_cur;
+        dst_cur = dst_next;
+        offsets(s + 2, src_next, dst_next);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        if (IN_PLACE) {  // all of this step has been read
             if (ctas > 1) cg::this_cluster().sync();
             else __syncthreads();
         }
-#pragma unroll
-        for (int i = 0; i < MV_UN; ++i) {
-            const int x = i * MV_THREADS + tid;
-            const int row = x / (2 * cpr), y = x - row * 2 * cpr;
-            if (to[i] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<char*>(y >= cpr ? a.v : a.k) + to[i]) = buf[i];
+        int row = row0, piece = piece0;
+        const uint4* st = ring + (s % MV_STAGES) * (MV_STAGE / 16);
+        for (int x = lane; x - lane < pieces; x += 32) {
+            const int64_t o = __shfl_sync(0xffffffffu, dst, row & 31);
+            if (x < pieces && o >= 0) *reinterpret_cast<uint4*>(base + o + piece * 16) = st[x];
+            row += drow;
+            piece += dpiece;
+            if (piece >= cpr) {
+                piece -= cpr;
+                ++row;
+            }
         }
+        __syncwarp();
     }
 }
 
-cudaError_t launch_cluster(const void* kern, unsigned grid, int cluster, int threads, size_t smem, cudaStream_t st,
-                           void** args) {
+cudaError_t launch(const void* kern, unsigned grid, int cluster, int threads, size_t smem, bool dependent,
+                   cudaStream_t st, void** args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
@@ -308,30 +364,38 @@ int evict_max_len() { return SE_MAX_CLUSTER * SE_MAX_SLICE; }
 
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     const int heads = a.B * a.Hkv;
+    // Slices of 2,048 sums (four for each thread), as long as the GPU holds the CTAs at once
+    // (four per SM); more than 8 CTAs only for slices that would not fit otherwise, or few heads.
     int C = 1;
-    while (C < 8 && (int64_t)C * 4096 < a.max_len && (int64_t)heads * C < 2 * sms) C *= 2;
+    while (C < SE_MAX_CLUSTER && (int64_t)C * 2048 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
     while ((int64_t)C * SE_MAX_SLICE < a.max_len) C *= 2;
     const size_t smem = sizeof(float) * (((size_t)a.max_len + C - 1) / C);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemLimit limit;  // the largest slice's, for every call
+    cudaError_t e = limit.allow((const void*)evict_select_kernel, (int)sizeof(float) * SE_MAX_SLICE);
     if (e == cudaSuccess && C > 8)
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<EvictArgs*>(&a)};
-    e = launch_cluster((const void*)evict_select_kernel, (unsigned)(heads * C), C, SE_THREADS, smem, st, args);
+    e = launch((const void*)evict_select_kernel, (unsigned)(heads * C), C, SE_THREADS, smem, false, st, args);
     if (e != cudaSuccess) return e;
-    const int cpr = a.row_bytes / 16;
-    int rows = MV_PIECES / (2 * cpr);
+    const int rows = (MV_STAGE / a.row_bytes < 32 ? MV_STAGE / a.row_bytes : 32) * MV_WARPS;  // of a CTA's step
     int ctas = 1;
+    const int ring = MV_WARPS * MV_STAGES * MV_STAGE;
+    void* margs[] = {const_cast<EvictArgs*>(&a), &ctas};
     if (a.dst_table) {
-        const int64_t all = (a.budget + rows - 1) / rows;
-        ctas = (int)all;
-        while (ctas > 1 && (int64_t)heads * ctas > 16LL * sms) ctas = (ctas + 1) / 2;
-    } else {
-        while (ctas < 8 && ctas * rows < a.budget && (int64_t)heads * ctas < 4LL * sms) ctas *= 2;
+        ctas = (a.budget + 2 * rows - 1) / (2 * rows);
+        static SmemLimit copy_limit;
+        e = copy_limit.allow((const void*)evict_move_kernel<false>, ring);
+        if (e != cudaSuccess) return e;
+        return launch((const void*)evict_move_kernel<false>, (unsigned)(2 * heads * ctas), 1, MV_THREADS, ring, true, st,
+                      margs);
     }
-    void* margs[] = {const_cast<EvictArgs*>(&a), &rows, &ctas};
-    return launch_cluster((const void*)evict_move_kernel, (unsigned)(heads * ctas), a.dst_table ? 1 : ctas, MV_THREADS, 0,
-                          st, margs);
+    while (ctas < 8 && ctas * rows < a.budget && (int64_t)2 * heads * ctas < 2LL * sms) ctas *= 2;
+    static SmemLimit place_limit;
+    e = place_limit.allow((const void*)evict_move_kernel<true>, ring);
+    if (e != cudaSuccess) return e;
+    return launch((const void*)evict_move_kernel<true>, (unsigned)(2 * heads * ctas), ctas, MV_THREADS, ring, true, st,
+                  margs);
 }
 
 }  // namespace tv

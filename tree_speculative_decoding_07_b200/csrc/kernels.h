@@ -4,7 +4,25 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace tv {
+
+// Dynamic shared memory that a kernel was allowed, per device, so that the
+// attribute is set once and not at every call.
+struct SmemLimit {
+    std::atomic<int> set[64] = {};
+    cudaError_t allow(const void* kern, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool known = dev >= 0 && dev < 64;
+        if (known && set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && known) set[dev].store(bytes, std::memory_order_release);
+        return e;
+    }
+};
 
 struct AttnArgs {
     const void* q;
