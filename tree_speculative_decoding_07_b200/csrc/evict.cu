@@ -7,11 +7,11 @@
 // order: token kept[r] moves to position r.
 //
 // evict_select_kernel: one cluster per (sequence, KV head).  Each CTA reads its
-// slice of the sums into shared memory once; a radix selection (digits of 11,
-// 11 and 10 bits of the order-preserving key, histograms joined through
-// distributed shared memory) finds the smallest kept key and how many of its
-// equals are kept; then each warp writes the positions of its part in order
-// (ballots), starting from the counts of the parts before it.
+// slice of the sums once and keeps them as order-preserving keys in shared memory;
+// a radix selection (digits of 11, 11 and 10 bits, the CTAs' counts added up
+// through distributed shared memory) finds the smallest kept key and how many
+// of its equals are kept; then each warp writes the positions of its part in
+// order, starting from the counts of the parts before it.
 //
 // evict_move_kernel: rows move from kept[r] to r.  In place a destination can
 // be another row's source, but never a later one's: src(r) >= r, and src rises
@@ -35,18 +35,21 @@ constexpr int SE_WARPS = SE_THREADS / 32;
 constexpr int SE_MAX_CLUSTER = 16;
 constexpr int SE_MAX_SLICE = 49152;  // sums in one CTA's shared memory (192 KB)
 constexpr int BINS = 2048;
-constexpr int SE_UN = 4;             // sums a thread loads at once
+constexpr int SE_UN = 4;             // 16-byte loads of sums that a thread has in flight
+constexpr int SE_STEP = 128;         // sums a warp handles at once, four neighbours per lane
 
 // Order-preserving key of a sum: larger sums, larger keys; NaN 0; -0 as +0.
 __device__ __forceinline__ uint32_t sum_key(float w) {
-    if (w != w) return 0;
     const uint32_t u = __float_as_uint(w + 0.0f);  // -0 + 0 = +0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return w != w ? 0u : u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float key_sum(uint32_t key) {
+    return __uint_as_float(key == 0 ? 0x7fc00000u : key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
 struct SelectShared {
     uint32_t own[BINS];         // this CTA's counts of the current digit
-    uint32_t total[3][BINS];    // the cluster's, added up by its CTAs
+    uint32_t total[3][BINS];    // the cluster's; CTA c keeps those of bins c * BINS / C and on
     uint32_t scan[SE_WARPS];
     uint2 warp_cnt[SE_WARPS];   // kept for certain, equal to the threshold
     uint2 cta_cnt;              // the CTA's sums of those, read by its peers
@@ -54,15 +57,19 @@ struct SelectShared {
     int bad;
 };
 
-__global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    extern __shared__ float s_w[];
-    __shared__ SelectShared s;
+__global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a, int vec) {
+    extern __shared__ __align__(16) uint32_t s_key[];
+    __shared__ __align__(16) SelectShared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int bh = blockIdx.x / C, b = bh / a.Hkv, h = bh - b * a.Hkv;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t L = a.lens[b];
+    if (tid == 0) s.bad = 0;
+    for (int i = tid; i < BINS / 4; i += SE_THREADS) reinterpret_cast<uint4*>(s.own)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 3 * BINS / 4; i += SE_THREADS)
+        reinterpret_cast<uint4*>(&s.total[0][0])[i] = make_uint4(0, 0, 0, 0);
     int32_t* kept = a.kept + (size_t)bh * a.budget;
     const bool lead = h == 0 && rank == 0 && tid == 0;
     if (L < 0 || L > a.max_len) {  // the same in every CTA of the cluster
@@ -73,32 +80,42 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
         for (int r = rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
         return;
     }
+    __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the totals are cleared
     const int n = L < a.budget ? L : a.budget;
     const bool cut = L > a.budget;
     const int want = cut ? a.budget - a.sink - a.recent : 0;
-    if (tid == 0) s.bad = 0;
-    if (want) {
-        for (int i = tid; i < BINS; i += SE_THREADS) s.own[i] = 0;
-        for (int i = tid; i < 3 * BINS; i += SE_THREADS) (&s.total[0][0])[i] = 0;
-    }
-    __syncthreads();
-    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the totals are cleared
+    // candidates: lo <= t < lo + span, as one unsigned comparison
+    const uint32_t lo = cut ? a.sink : 0, span = cut ? L - a.recent - a.sink : 0;
     // this CTA's slice of the sums
-    const int slice = (L + C - 1) / C;
-    const int t0 = min(L, rank * slice), t1 = min(L, t0 + slice);
-    const float* w = a.weights + (size_t)bh * a.weight_stride;
-    const int lo = min(a.sink, L), hi = max(lo, L - a.recent);  // candidates [lo, hi)
-    for (int t = t0 + tid; t < t1; t += SE_UN * SE_THREADS) {
-        float x[SE_UN];
-#pragma unroll
-        for (int i = 0; i < SE_UN; ++i) x[i] = t + i * SE_THREADS < t1 ? w[t + i * SE_THREADS] : 0.f;
+    const int slice = ((L + C - 1) / C + SE_STEP - 1) / SE_STEP * SE_STEP;
+    const int t0 = min(L, rank * slice), t1 = min(L, t0 + slice), len = t1 - t0;
+    const float* w = a.weights + (size_t)bh * a.weight_stride + t0;
+#pragma unroll 1
+    for (int y0 = tid * 4; y0 < len; y0 += SE_UN * 4 * SE_THREADS) {
+        float4 x[SE_UN];
 #pragma unroll
         for (int i = 0; i < SE_UN; ++i) {
-            const int y = t + i * SE_THREADS;
-            if (y < t1) {
-                s_w[y - t0] = x[i];
-                if (want && y >= lo && y < hi) atomicAdd(&s.own[sum_key(x[i]) >> 21], 1u);
+            const int y = y0 + i * 4 * SE_THREADS;
+            if (vec && y + 4 <= len) {
+                x[i] = *reinterpret_cast<const float4*>(w + y);
+            } else {
+                x[i].x = y < len ? w[y] : 0.f;
+                x[i].y = y + 1 < len ? w[y + 1] : 0.f;
+                x[i].z = y + 2 < len ? w[y + 2] : 0.f;
+                x[i].w = y + 3 < len ? w[y + 3] : 0.f;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < SE_UN; ++i) {
+            const int y = y0 + i * 4 * SE_THREADS;
+            if (y >= len) break;
+            const uint4 k = make_uint4(sum_key(x[i].x), sum_key(x[i].y), sum_key(x[i].z), sum_key(x[i].w));
+            *reinterpret_cast<uint4*>(s_key + y) = k;
+            const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (want && (uint32_t)(t0 + y + e) - lo < span && y + e < len) atomicAdd(&s.own[ks[e] >> 21], 1u);
         }
     }
     // block ids of the span that is read and of the one that is written
@@ -116,38 +133,44 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
     }
     __syncthreads();
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    uint32_t prefix = 0, left = (uint32_t)want;  // key bits found so far; how many are still to be taken
+    // the smallest kept key, and how many of its equals are kept; none when only sink and recent are
+    uint32_t threshold = want ? 0u : 0xffffffffu, left = (uint32_t)want;
     if (want) {
-        constexpr int PER = BINS / SE_THREADS;
+        constexpr int PER = 4;
+        static_assert(PER * SE_THREADS == BINS, "four bins per thread");
+        const int bin0 = BINS - PER - PER * tid;  // bins from the top down: this thread's are bin0 .. bin0 + 3
+        const int owner = bin0 / (BINS / C);
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             if (pass) {
-                const int shift = pass == 1 ? 10 : 0, keep_shift = pass == 1 ? 21 : 10;
+                const int shift = pass == 1 ? 10 : 0, done = pass == 1 ? 21 : 10;
                 const uint32_t mask = pass == 1 ? 2047u : 1023u;
-                for (int t = max(t0, lo) + tid; t < min(t1, hi); t += SE_THREADS) {
-                    const uint32_t key = sum_key(s_w[t - t0]);
-                    if ((key ^ prefix) >> keep_shift == 0) atomicAdd(&s.own[(key >> shift) & mask], 1u);
+#pragma unroll 1
+                for (int y = tid * 4; y < len; y += 4 * SE_THREADS) {
+                    const uint4 k = *reinterpret_cast<const uint4*>(s_key + y);
+                    const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((ks[e] ^ threshold) >> done == 0 && (uint32_t)(t0 + y + e) - lo < span && y + e < len)
+                            atomicAdd(&s.own[(ks[e] >> shift) & mask], 1u);
                 }
                 __syncthreads();
             }
-            // every CTA adds its counts (few bins hold any) to each one's totals
-            uint32_t cnt[PER], sum = 0;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const int bin = BINS - 1 - (PER * tid + e);
-                cnt[e] = s.own[bin];
-                if (C > 1 && cnt[e])
-                    for (int c = 0; c < C; ++c) atomicAdd(cluster.map_shared_rank(&s.total[pass][bin], c), cnt[e]);
-                s.own[bin] = 0;
-            }
+            uint4 cnt = *reinterpret_cast<const uint4*>(&s.own[bin0]);
             if (C > 1) {
+                // bins that hold any go to the CTA that keeps their totals; then everybody reads all totals
+                if (cnt.x | cnt.y | cnt.z | cnt.w) {
+                    uint32_t* to = cluster.map_shared_rank(&s.total[pass][bin0], owner);
+                    if (cnt.x) atomicAdd(to, cnt.x);
+                    if (cnt.y) atomicAdd(to + 1, cnt.y);
+                    if (cnt.z) atomicAdd(to + 2, cnt.z);
+                    if (cnt.w) atomicAdd(to + 3, cnt.w);
+                }
                 cluster.sync();
-#pragma unroll
-                for (int e = 0; e < PER; ++e) cnt[e] = s.total[pass][BINS - 1 - (PER * tid + e)];
+                cnt = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s.total[pass][bin0], owner));
             }
-            // bins from the top down: thread i holds bins BINS - 1 - PER i and below
-#pragma unroll
-            for (int e = 0; e < PER; ++e) sum += cnt[e];
+            *reinterpret_cast<uint4*>(&s.own[bin0]) = make_uint4(0, 0, 0, 0);
+            const uint32_t sum = cnt.x + cnt.y + cnt.z + cnt.w;
             uint32_t inc = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -158,34 +181,41 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             __syncthreads();
             uint32_t before = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s.scan[lane] : 0u);
             if (before < left && left <= before + sum) {
+                const uint32_t c[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
 #pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    if (before < left && left <= before + cnt[e]) {
-                        s.digit = BINS - 1 - (PER * tid + e);
+                for (int e = 0; e < 4; ++e) {
+                    if (before < left && left <= before + c[e]) {
+                        s.digit = bin0 + 3 - e;
                         s.above = before;
                     }
-                    before += cnt[e];
+                    before += c[e];
                 }
             }
             __syncthreads();
-            prefix |= s.digit << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
+            threshold |= s.digit << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
             left -= s.above;
         }
     }
-    // prefix is now the smallest kept key, left how many of its equals are kept
-    auto classify = [&](int t, float x, bool& sure, bool& equal) {
-        const uint32_t key = sum_key(x);
-        sure = !cut || t < lo || t >= hi || (want && key > prefix);
-        equal = !sure && want && key == prefix;
+    // kept for certain: not a candidate, or above the threshold; x in the low half, equals in the high one
+    auto classify = [&](int y, const uint32_t* ks, uint32_t* f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool sure = (uint32_t)(t0 + y + e) - lo >= span || ks[e] > threshold;
+            f[e] = y + e >= len ? 0u : sure ? 1u : ks[e] == threshold ? 0x10000u : 0u;
+        }
     };
-    const int per = ((t1 - t0 + SE_WARPS - 1) / SE_WARPS + 31) / 32 * 32;
-    const int w0 = min(t1, t0 + warp * per), w1 = min(t1, w0 + per);
+    const int per = ((len + SE_WARPS - 1) / SE_WARPS + SE_STEP - 1) / SE_STEP * SE_STEP;
+    const int w0 = min(len, warp * per), w1 = min(len, w0 + per);  // this warp's part of the slice
     uint32_t nk = 0, ne = 0;
-    for (int t = w0 + lane; t < w1; t += 32) {
-        bool k, e;
-        classify(t, s_w[t - t0], k, e);
-        nk += k;
-        ne += e;
+#pragma unroll 1
+    for (int y = w0 + lane * 4; y < w1; y += SE_STEP) {
+        const uint4 k = *reinterpret_cast<const uint4*>(s_key + y);
+        const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+        uint32_t f[4];
+        classify(y, ks, f);
+        const uint32_t c = f[0] + f[1] + f[2] + f[3];
+        nk += c & 0xffffu;
+        ne += c >> 16;
     }
     nk = __reduce_add_sync(0xffffffffu, nk);
     ne = __reduce_add_sync(0xffffffffu, ne);
@@ -222,21 +252,33 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
         for (int r = rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
     } else {
         float* wo = a.weights_out ? a.weights_out + (size_t)bh * a.weight_stride : nullptr;
-        const uint32_t below = (1u << lane) - 1;
-        for (int t = w0; t < w1; t += 32) {
-            const bool in = t + lane < w1;
-            const float x = in ? s_w[t + lane - t0] : 0.f;
-            bool k, e;
-            classify(t + lane, x, k, e);
-            const uint32_t kb = __ballot_sync(0xffffffffu, in && k), eb = __ballot_sync(0xffffffffu, in && e);
-            const uint32_t my_eq = be + __popc(eb & below);  // equals before this one
-            if (in && (k || (e && my_eq < left))) {
-                const uint32_t r = bk + __popc(kb & below) + min(my_eq, left);
-                kept[r] = t + lane;
-                if (wo) wo[r] = x;
+#pragma unroll 1
+        for (int y0 = w0; y0 < w1; y0 += SE_STEP) {
+            const int y = y0 + lane * 4;
+            const uint4 kv = y < w1 ? *reinterpret_cast<const uint4*>(s_key + y) : make_uint4(0, 0, 0, 0);
+            const uint32_t ks[4] = {kv.x, kv.y, kv.z, kv.w};
+            uint32_t f[4];
+            classify(y, ks, f);
+            const uint32_t c = f[0] + f[1] + f[2] + f[3];
+            uint32_t inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += z;
             }
-            bk += __popc(kb);
-            be += __popc(eb);
+            uint32_t k = bk + ((inc - c) & 0xffffu), q = be + ((inc - c) >> 16);  // before this lane's four
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool take = f[e] == 1u || (f[e] && q < left);
+                const uint32_t r = k + min(q, left);
+                if (take) kept[r] = t0 + y + e;
+                if (take && wo) wo[r] = key_sum(ks[e]);
+                k += f[e] & 1u;
+                q += f[e] >> 16;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+            bk += all & 0xffffu;
+            be += all >> 16;
         }
         for (int r = n + rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
         if (wo)
@@ -247,9 +289,9 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no peer reads this CTA's counts any more
 }
 
-constexpr int MV_WARPS = 4;
+constexpr int MV_WARPS = 8;
 constexpr int MV_THREADS = MV_WARPS * 32;
-constexpr int MV_STAGE = 8192;  // bytes of a warp's step
+constexpr int MV_STAGE = 4096;  // bytes of a warp's step
 constexpr int MV_STAGES = 2;
 
 __device__ __forceinline__ void mv_async16(void* dst, const void* src) {
@@ -364,24 +406,31 @@ int evict_max_len() { return SE_MAX_CLUSTER * SE_MAX_SLICE; }
 
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     const int heads = a.B * a.Hkv;
-    // Slices of 2,048 sums (four for each thread), as long as the GPU holds the CTAs at once
-    // (four per SM); more than 8 CTAs only for slices that would not fit otherwise, or few heads.
+    // Slices of 2,048 sums (four for each thread), as long as the GPU holds twice the CTAs at
+    // four per SM.  At 128K sums and 8 heads clusters of 4, 8 and 16 took (with the move) 63, 50
+    // and 49 us; above 8, which not every part of the GPU can place, only for what would not fit.
     int C = 1;
-    while (C < SE_MAX_CLUSTER && (int64_t)C * 2048 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
+    while (C < 8 && (int64_t)C * 2048 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
     while ((int64_t)C * SE_MAX_SLICE < a.max_len) C *= 2;
-    const size_t smem = sizeof(float) * (((size_t)a.max_len + C - 1) / C);
+    const size_t smem = sizeof(uint32_t) * ((((size_t)a.max_len + C - 1) / C + SE_STEP - 1) / SE_STEP * SE_STEP);
     static SmemLimit limit;  // the largest slice's, for every call
     cudaError_t e = limit.allow((const void*)evict_select_kernel, (int)sizeof(float) * SE_MAX_SLICE);
     if (e == cudaSuccess && C > 8)
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    void* args[] = {const_cast<EvictArgs*>(&a)};
+    int vec = a.weight_stride % 4 == 0 && !(reinterpret_cast<uintptr_t>(a.weights) & 15);
+    void* args[] = {const_cast<EvictArgs*>(&a), &vec};
     e = launch((const void*)evict_select_kernel, (unsigned)(heads * C), C, SE_THREADS, smem, false, st, args);
     if (e != cudaSuccess) return e;
     const int rows = (MV_STAGE / a.row_bytes < 32 ? MV_STAGE / a.row_bytes : 32) * MV_WARPS;  // of a CTA's step
     int ctas = 1;
     const int ring = MV_WARPS * MV_STAGES * MV_STAGE;
     void* margs[] = {const_cast<EvictArgs*>(&a), &ctas};
+    // Steps of 4 KB in 8 warps.  Selection and move together, four cases (4K in place, 8 x 8K
+    // copied, 128K copied, 32 mixed in place): 16.9, 59, 48 and 240 us; 8 KB in 4 warps 16.9, 62,
+    // 50 and 257; 4 KB in 4 warps 19.2, 59, 48 and 256; 8 KB in 8 warps 18.1, 71, 54 and 318.
+    // Copies: two steps per CTA (one 64 us at 8 x 8K, three 60).  In place: a cluster of up to 8,
+    // while the GPU has no 8 CTAs per SM (4: 258 us on the mixed case, 16: 254).
     if (a.dst_table) {
         ctas = (a.budget + 2 * rows - 1) / (2 * rows);
         static SmemLimit copy_limit;
@@ -390,7 +439,7 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
         return launch((const void*)evict_move_kernel<false>, (unsigned)(2 * heads * ctas), 1, MV_THREADS, ring, true, st,
                       margs);
     }
-    while (ctas < 8 && ctas * rows < a.budget && (int64_t)2 * heads * ctas < 2LL * sms) ctas *= 2;
+    while (ctas < 8 && ctas * rows < a.budget && (int64_t)2 * heads * ctas < 8LL * sms) ctas *= 2;
     static SmemLimit place_limit;
     e = place_limit.allow((const void*)evict_move_kernel<true>, ring);
     if (e != cudaSuccess) return e;
