@@ -9,8 +9,8 @@
 // one by less than 2^-35.  What is left lies in [-1/2, 1/2] turns and goes to
 // fp32 sincospi.  The cosines and sines of a node serve all of its heads.
 //
-// One CTA per node.  While the first R/2 threads form the angles, every
-// thread's first loads are already under way.  Bound: HBM (each row is read
+// One CTA per node.  Every thread's first loads are under way while one thread
+// looks up where the rows go and the first R/2 threads form the angles.  Bound: HBM (each row is read
 // once and written once).
 #include "kernels.h"
 #include "tv_common.cuh"
@@ -18,7 +18,8 @@
 namespace tv {
 namespace {
 
-constexpr int RO_THREADS = 256;
+constexpr int RO_THREADS = 128;
+constexpr int RO_UN = 3;  // heads of a thread whose loads are under way before the angles are known
 
 // 16 bytes as fp32 values, and back
 template <typename T> struct Pack;
@@ -86,20 +87,44 @@ __device__ __forceinline__ int node_depth(const int32_t* parent, int j) {
     return parent[0] == -1 ? depth : -1;
 }
 
-template <typename T>
+template <typename T, bool INTER>
 __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int PN = Pack<T>::N;
-    __shared__ float s_cos[128], s_sin[128];
+    constexpr int NF = INTER ? PN / 2 : PN;  // frequencies of a thread's pieces
+    __shared__ __align__(16) float s_cos[128], s_sin[128];
     __shared__ long long s_off;
-    __shared__ int s_bad, s_depth;
+    __shared__ int s_bad;
     const int tid = threadIdx.x, b = blockIdx.x / a.N, j = blockIdx.x - b * a.N;
     bool bad_count;
     const int n = seq_nodes(a.counts, b, a.N, bad_count);
     if (j >= n) return;
     const int L = a.prefix_lens[b];
-    if (tid == 0) {
-        int bad = 0, depth = j;
-        long long off = -1;
+    const size_t node = (size_t)b * a.N + j;
+    // A thread keeps to one place of the rows: piece i (and i + Rp / 2), of the heads
+    // g, g + groups, ...: the query heads, then the key heads.
+    const int Dp = a.D / PN, Rp = a.rot / PN;  // 16-byte pieces of a row; rotated pieces
+    const int units = INTER ? Dp : Dp - Rp / 2, groups = RO_THREADS / units;
+    const int g = tid / units, i = tid - g * units;
+    const bool turns_here = i < (INTER ? Rp : Rp / 2);
+    const int at = INTER || turns_here ? i : i + Rp / 2;  // past the rotated part: one piece
+    const int qh = a.q ? a.Hq : 0, heads = g < groups ? qh + a.Hkv : 0;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + node * a.q_stride) + at;
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + node * a.k_stride) + at;
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + node * a.v_stride);
+    auto load = [&](int h, uint4& u, uint4& w) {
+        const uint4* src = h < qh ? q + h * Dp : k + (h - qh) * Dp;
+        u = src[0];
+        if (!INTER && turns_here) w = src[Rp / 2];
+    };
+    uint4 u[RO_UN], w[RO_UN], vv = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < RO_UN; ++e)
+        if (g + e * groups < heads) load(g + e * groups, u[e], w[e]);
+    if (tid < a.Hkv * Dp) vv = v[tid];
+
+    if (tid == RO_THREADS - 1) {  // where the rows go
+        int bad = 0;
+        long long off = 0;
         if (bad_count || L < 0 || (long long)L + n > (long long)a.c.max_blocks * a.c.block_size) {
             bad = TV_ERR_INVALID_ARG;
         } else {
@@ -107,100 +132,98 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constan
             const int id = a.c.table[(size_t)b * a.c.max_blocks + blk];
             if (id < 0 || id >= a.c.num_blocks) bad = TV_ERR_BLOCK_TABLE;
             else off = (long long)id * a.c.block_stride + (long long)(t - blk * a.c.block_size) * a.c.token_stride;
-            if (a.parent) {
-                depth = node_depth(a.parent + (size_t)b * a.N, j);
-                if (depth < 0) bad = TV_ERR_TREE;
-            }
         }
-        s_bad = bad;
         s_off = off;
-        s_depth = depth;
-        if (bad) report(a.status, bad);
+        s_bad = bad;
+    }
+    int depth = j;
+    if (a.parent) depth = node_depth(a.parent + (size_t)b * a.N, j);
+    if (tid < a.rot / 2) {
+        const int ax = a.axis_of_pair[tid];
+        double pos;
+        if (a.positions) pos = (double)a.positions[((size_t)ax * a.B + b) * a.N + j];
+        else pos = (double)(a.position_base ? a.position_base[b] : L) + (double)depth;
+        const double turns = pos * (double)a.inv_freq[tid] * 0.15915494309189533577;
+        float sn, cs;
+        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
+        s_cos[tid] = cs;
+        s_sin[tid] = sn;
     }
     __syncthreads();
-    const int bad = s_bad;
-    if (!bad) {
-        for (int i = tid; i < a.rot / 2; i += RO_THREADS) {
-            const int ax = a.axis_of_pair[i];
-            double pos;
-            if (a.positions) pos = (double)a.positions[((size_t)ax * a.B + b) * a.N + j];
-            else pos = (double)(a.position_base ? a.position_base[b] : L) + (double)s_depth;
-            const double turns = pos * (double)a.inv_freq[i] * 0.15915494309189533577;
-            float sn, cs;
-            sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
-            s_cos[i] = cs;
-            s_sin[i] = sn;
-        }
-    }
-    __syncthreads();
-    const int Dp = a.D / PN, Rp = a.rot / PN;    // 16-byte pieces of a row; rotated pieces
-    const size_t node = (size_t)b * a.N + j;
-    const uint4* q = a.q ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + node * a.q_stride) : nullptr;
+    const int bad = s_bad ? s_bad : depth < 0 ? TV_ERR_TREE : 0;
     uint4* qo = reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + node * (size_t)a.Hq * a.D);
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + node * a.k_stride);
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + node * a.v_stride);
-    if (bad) {
-        if (q) {
-            float nanv[PN];
+    if (bad) {  // NaN queries, nothing else
+        if (tid == 0) report(a.status, bad);
+        float x[PN];
 #pragma unroll
-            for (int e = 0; e < PN; ++e) nanv[e] = __int_as_float(0x7fc00000);
-            for (int i = tid; i < a.Hq * Dp; i += RO_THREADS) qo[i] = Pack<T>::put(nanv);
-        }
-    } else {
-        char* ck = static_cast<char*>(a.cache_k) + s_off;
-        char* cv = static_cast<char*>(a.cache_v) + s_off;
-        const int heads = (q ? a.Hq : 0) + a.Hkv;
-        // split halves: a unit is the pieces i and i + R/2; neighbouring pairs: one piece
-        const int units = a.interleaved ? Dp : Dp - Rp / 2;
-        for (int x = tid; x < heads * units; x += RO_THREADS) {
-            const int hh = x / units, i = x - hh * units;
-            const bool isq = q && hh < a.Hq;
-            const int h = isq || !q ? hh : hh - a.Hq;
-            const uint4* src = (isq ? q : k) + (size_t)h * Dp;
-            uint4* dst = isq ? qo + (size_t)h * Dp : reinterpret_cast<uint4*>(ck + h * a.c.head_stride);
-            float f[PN], g[PN], r[PN];
-            if (a.interleaved) {
-                const uint4 u = src[i];
-                if (i >= Rp) { dst[i] = u; continue; }
-                Pack<T>::get(u, f);
+        for (int e = 0; e < PN; ++e) x[e] = __int_as_float(0x7fc00000);
+        for (int y = tid; y < qh * Dp; y += RO_THREADS) qo[y] = Pack<T>::put(x);
+        return;
+    }
+    char* ck = static_cast<char*>(a.cache_k) + s_off;
+    char* cv = static_cast<char*>(a.cache_v) + s_off;
+    float cs[NF], sn[NF];
+    if (turns_here) {
 #pragma unroll
-                for (int e = 0; e < PN; e += 2) {
-                    const float cs = s_cos[(i * PN + e) / 2], sn = s_sin[(i * PN + e) / 2];
-                    r[e] = f[e] * cs - f[e + 1] * sn;
-                    r[e + 1] = f[e] * sn + f[e + 1] * cs;
-                }
-                dst[i] = Pack<T>::put(r);
-            } else if (i < Rp / 2) {
-                const uint4 u = src[i], w = src[i + Rp / 2];
-                Pack<T>::get(u, f);
-                Pack<T>::get(w, g);
-                float r2[PN];
-#pragma unroll
-                for (int e = 0; e < PN; ++e) {
-                    const float cs = s_cos[i * PN + e], sn = s_sin[i * PN + e];
-                    r[e] = f[e] * cs - g[e] * sn;
-                    r2[e] = f[e] * sn + g[e] * cs;
-                }
-                dst[i] = Pack<T>::put(r);
-                dst[i + Rp / 2] = Pack<T>::put(r2);
-            } else {
-                dst[i + Rp / 2] = src[i + Rp / 2];  // past the rotated part
-            }
-        }
-        for (int x = tid; x < a.Hkv * Dp; x += RO_THREADS) {
-            const int h = x / Dp, i = x - h * Dp;
-            reinterpret_cast<uint4*>(cv + h * a.c.head_stride)[i] = v[(size_t)h * Dp + i];
+        for (int e = 0; e < NF; ++e) {
+            cs[e] = s_cos[i * NF + e];
+            sn[e] = s_sin[i * NF + e];
         }
     }
+    auto store = [&](int h, uint4 u, uint4 w) {
+        uint4* dst = h < qh ? qo + h * Dp : reinterpret_cast<uint4*>(ck + (h - qh) * a.c.head_stride);
+        if (turns_here) {
+            float f[PN];
+            Pack<T>::get(u, f);
+            if constexpr (INTER) {
+#pragma unroll
+                for (int e = 0; e < NF; ++e) {
+                    const float x = f[2 * e], y = f[2 * e + 1];
+                    f[2 * e] = x * cs[e] - y * sn[e];
+                    f[2 * e + 1] = x * sn[e] + y * cs[e];
+                }
+            } else {
+                float z[PN];
+                Pack<T>::get(w, z);
+#pragma unroll
+                for (int e = 0; e < NF; ++e) {
+                    const float x = f[e], y = z[e];
+                    f[e] = x * cs[e] - y * sn[e];
+                    z[e] = x * sn[e] + y * cs[e];
+                }
+                dst[at + Rp / 2] = Pack<T>::put(z);
+            }
+            u = Pack<T>::put(f);
+        }
+        dst[at] = u;
+    };
+#pragma unroll
+    for (int e = 0; e < RO_UN; ++e)
+        if (g + e * groups < heads) store(g + e * groups, u[e], w[e]);
+#pragma unroll 1
+    for (int h = g + RO_UN * groups; h < heads; h += groups) {
+        load(h, u[0], w[0]);
+        store(h, u[0], w[0]);
+    }
+#pragma unroll 1
+    for (int y = tid; y < a.Hkv * Dp; y += RO_THREADS) {
+        const int h = y / Dp;
+        reinterpret_cast<uint4*>(cv + h * a.c.head_stride)[y - h * Dp] = y == tid ? vv : v[y];
+    }
+}
+
+template <typename T> void launch(const RotaryArgs& a, unsigned grid, cudaStream_t st) {
+    if (a.interleaved) rotary_kernel<T, true><<<grid, RO_THREADS, 0, st>>>(a);
+    else rotary_kernel<T, false><<<grid, RO_THREADS, 0, st>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st) {
     const unsigned grid = (unsigned)a.B * (unsigned)a.N;  // fits: checked by the caller
-    if (dtype == TV_BF16) rotary_kernel<__nv_bfloat16><<<grid, RO_THREADS, 0, st>>>(a);
-    else if (dtype == TV_F16) rotary_kernel<__half><<<grid, RO_THREADS, 0, st>>>(a);
-    else rotary_kernel<float><<<grid, RO_THREADS, 0, st>>>(a);
+    if (dtype == TV_BF16) launch<__nv_bfloat16>(a, grid, st);
+    else if (dtype == TV_F16) launch<__half>(a, grid, st);
+    else launch<float>(a, grid, st);
     return cudaGetLastError();
 }
 
