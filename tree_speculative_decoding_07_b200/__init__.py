@@ -534,8 +534,8 @@ def _addr(t):
 
 def _on_gpu(stream, first, others):
     """The GPU that every tensor has to lie on, the stream to run on as an address, and the
-    contexts to enter for it (None: the call's GPU and stream are the current ones).  What is
-    allocated inside them belongs to the stream that the kernels run on."""
+    context to enter for it (None: the call's GPU and stream are the current ones).  What is
+    allocated inside it belongs to the stream that the kernels run on."""
     import torch
     at = first.get_device()
     if at < 0:
@@ -545,7 +545,7 @@ def _on_gpu(stream, first, others):
             raise ValueError(f"all tensors must be on one GPU: {first.device} and {t.device}")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(at)
-        return raw, None if torch.cuda.current_device() == at else torch.cuda.device(at)
+        return raw, None if torch._C._cuda_getDevice() == at else torch.cuda.device(at)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=first.device)
     elif stream.device != first.device:
@@ -553,18 +553,15 @@ def _on_gpu(stream, first, others):
     return stream.cuda_stream, torch.cuda.stream(stream)  # makes its GPU current too
 
 
-def _want(name, t, dtype, shape, optional=False):
+def _want(name, t, dtype, shape):
     """A contiguous tensor of the given type and shape."""
-    if t is None:
-        if not optional:
-            raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 _cache_types: dict = {}
@@ -616,6 +613,21 @@ def _row_strides(name, c):
     return strides
 
 
+# Descriptors by the values of their fields: shared by calls and threads, never changed.
+
+@functools.lru_cache(maxsize=256)
+def _cache_call(*fields):
+    desc = TvCacheDesc(*fields)
+    return desc, ctypes.byref(desc)
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_call(*fields, axes=b""):
+    rot = TvRotaryDesc(*fields)
+    ctypes.memmove(rot.axis_of_pair, axes, len(axes))
+    return rot, ctypes.byref(rot)
+
+
 @functools.lru_cache(maxsize=256)
 def _decode_call(gpu, with_weights, *fields):
     """Descriptor and workspace size of a decode call of these sizes on this GPU (current)."""
@@ -660,7 +672,7 @@ def _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_
         _want("attn_weights", attn_weights, torch.float32, (B, fields[2], weight_stride))
     desc, ref, ws_bytes = _decode_call(q.get_device(), attn_weights is not None, *fields, q_stride, weight_stride)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q) if not q_stride else torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
     else:
         _want("out", out, q.dtype, (B, Hq, D))
     if lse is None:
@@ -704,9 +716,11 @@ def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, r
     B, Hkv, budget = fields[0], fields[2], int(budget)
     _want("kv_lens", kv_lens, torch.int32, (B,))
     _want("weights", weights, torch.float32, (B, Hkv, weights.shape[-1]))
-    _want("weights_out", weights_out, torch.float32, weights.shape, optional=True)
-    _want("dst_block_table", dst_block_table, torch.int32, block_table.shape, optional=True)
-    desc = TvCacheDesc(*fields, 0, weights.shape[-1])
+    if weights_out is not None:
+        _want("weights_out", weights_out, torch.float32, weights.shape)
+    if dst_block_table is not None:
+        _want("dst_block_table", dst_block_table, torch.int32, block_table.shape)
+    ref = _cache_call(*fields, 0, weights.shape[-1])[1]
     if kept is None:
         kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
     else:
@@ -715,7 +729,7 @@ def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, r
         new_kv_lens = torch.empty_like(kv_lens)
     else:
         _want("new_kv_lens", new_kv_lens, torch.int32, (B,))
-    s = lib().tv_evict_cache(ctypes.byref(desc), budget, int(sink), int(recent), k_cache.data_ptr(),
+    s = lib().tv_evict_cache(ref, budget, int(sink), int(recent), k_cache.data_ptr(),
                              v_cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), weights.data_ptr(),
                              _addr(dst_block_table), _addr(weights_out), kept.data_ptr(), new_kv_lens.data_ptr(),
                              _addr(dev_status), raw)
@@ -724,15 +738,16 @@ def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, r
     return new_kv_lens, kept
 
 
-def _node_stride(name, t):
+def _node_stride(name, t, B, N, H, D):
     """Elements between consecutive nodes of [B][N][H][D]: heads contiguous, sequences N nodes apart."""
-    B, N, H, D = t.shape
     if t.is_contiguous():
         return 0
-    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D):
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: the heads of a node must be contiguous")
-    st = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else 0)
-    if B > 1 and N > 1 and t.stride(0) != N * st:
+    if N == 1:
+        return sb if B > 1 else 0
+    if B > 1 and sb != N * st:
         raise ValueError(f"{name}: sequences must lie num_nodes nodes apart")
     return st
 
@@ -759,45 +774,53 @@ def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=N
 def _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
             position_base, axis_of_pair, interleaved, node_counts, dev_status):
     import torch
-    if k.dim() != 4 or v.shape != k.shape or k.dtype != k_cache.dtype or v.dtype != k.dtype:
+    if k.dim() != 4 or v.shape != k.shape or k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
         raise TypeError("k and v must be [batch][nodes][num_kv_heads][head_dim] of the caches' type")
     B, N, Hkv, D = k.shape
     Hq, q_stride = Hkv, 0
     if q is not None:
-        if q.dim() != 4 or q.dtype != k.dtype or q.shape[:2] != k.shape[:2] or q.shape[3] != D:
+        Hq = q.shape[2] if q.dim() == 4 else 0
+        if q.dtype != k.dtype or q.shape != (B, N, Hq, D):
             raise TypeError("q must be [batch][nodes][num_q_heads][head_dim] of k's type")
-        Hq = q.shape[2]
-        q_stride = _node_stride("q", q)
+        q_stride = _node_stride("q", q, B, N, Hq, D)
     fields = _cache_fields(k_cache, v_cache, block_table, Hq, 0.0, 0)
     if fields[0] != B or fields[2] != Hkv or fields[3] != D:
         raise ValueError("k, block_table and the caches disagree on batch, heads or head_dim")
-    pairs = inv_freq.numel()
+    pairs, axes, num_axes, counts = inv_freq.numel(), b"", 1, None
+    if pairs > 128:
+        raise ValueError("inv_freq must have at most 128 entries")
     _want("inv_freq", inv_freq, torch.float32, (pairs,))
     _want("prefix_lens", prefix_lens, torch.int32, (B,))
-    _want("position_base", position_base, torch.int32, (B,), optional=True)
-    _want("parent_idx", parent_idx, torch.int32, (B, N), optional=True)
-    _want("node_counts", node_counts, torch.int32, (B,), optional=True)
-    rot = TvRotaryDesc(N, 2 * pairs, int(bool(interleaved)), 1, q_stride, _node_stride("k", k), _node_stride("v", v),
-                       _addr(node_counts))
+    if position_base is not None:
+        _want("position_base", position_base, torch.int32, (B,))
+    if parent_idx is not None:
+        _want("parent_idx", parent_idx, torch.int32, (B, N))
+    if node_counts is not None:
+        _want("node_counts", node_counts, torch.int32, (B,))
+        counts = node_counts.data_ptr()
     if axis_of_pair is not None:
         axes = bytes(axis_of_pair)
-        if len(axes) != pairs or pairs > 128:
-            raise ValueError("axis_of_pair must have an entry for each of inv_freq (at most 128)")
-        ctypes.memmove(rot.axis_of_pair, axes, pairs)
-        rot.num_axes = max(axes, default=0) + 1
+        if len(axes) != pairs:
+            raise ValueError("axis_of_pair must have an entry for each of inv_freq")
+        num_axes = max(axes, default=0) + 1
     if positions is not None:
-        _want("positions", positions, torch.int32, (positions.shape[0], B, N))
-        if positions.shape[0] < rot.num_axes:
+        if positions.shape[0] < num_axes:
             raise ValueError("axis_of_pair names an axis that positions lacks")
-        rot.num_axes = positions.shape[0]
+        num_axes = positions.shape[0]
+        _want("positions", positions, torch.int32, (num_axes, B, N))
+    rot = (N, 2 * pairs, 1 if interleaved else 0, num_axes, q_stride, _node_stride("k", k, B, N, Hkv, D),
+           _node_stride("v", v, B, N, Hkv, D), counts)
+    # with counts, their address is in the descriptor: it is this call's own
+    rot, rot_ref = (_rotary_call if counts is None else _rotary_call.__wrapped__)(*rot, axes=axes)
+    ref = _cache_call(*fields, 0, 0)[1]
     if q_out is not None:
         _want("q_out", q_out, k.dtype, (B, N, Hq, D))
     elif q is not None:
         q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-    s = lib().tv_rotary_write(ctypes.byref(TvCacheDesc(*fields, 0, 0)), ctypes.byref(rot), _addr(q), k.data_ptr(),
-                              v.data_ptr(), inv_freq.data_ptr(), _addr(parent_idx), _addr(positions),
-                              _addr(position_base), prefix_lens.data_ptr(), block_table.data_ptr(), _addr(q_out),
-                              k_cache.data_ptr(), v_cache.data_ptr(), _addr(dev_status), raw)
+    s = lib().tv_rotary_write(ref, rot_ref, _addr(q), k.data_ptr(), v.data_ptr(), inv_freq.data_ptr(),
+                              _addr(parent_idx), _addr(positions), _addr(position_base), prefix_lens.data_ptr(),
+                              block_table.data_ptr(), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                              _addr(dev_status), raw)
     if s != TV_OK:
         raise TreeVerifyError(s, "tv_rotary_write")
     return q_out

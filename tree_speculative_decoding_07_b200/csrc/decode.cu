@@ -327,10 +327,18 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                 for (int j = 0; j < NT; ++j) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int hd = j * 8 + (lane % 4) * 2 + e;
                         c[j][e] = in0 ? c[j][e] * a.scale_log2 : -INFINITY;
                         c[j][2 + e] = in1 ? c[j][2 + e] * a.scale_log2 : -INFINITY;
-                        if (sc && hd < heads) {
+                    }
+                    const int hd0 = j * 8 + (lane % 4) * 2;
+                    if (sc && !(a.GS & 1) && hd0 < heads) {  // then an even number of heads, and pairs are aligned
+                        if (in0) *reinterpret_cast<float2*>(sc + r0 * a.GS + hd0) = make_float2(c[j][0], c[j][1]);
+                        if (in1) *reinterpret_cast<float2*>(sc + (r0 + 8) * a.GS + hd0) = make_float2(c[j][2], c[j][3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int hd = hd0 + e;
+                        if (sc && (a.GS & 1) && hd < heads) {
                             if (in0) sc[r0 * a.GS + hd] = c[j][e];
                             if (in1) sc[(r0 + 8) * a.GS + hd] = c[j][2 + e];
                         }
@@ -551,11 +559,12 @@ __device__ __forceinline__ int find_seq(const int32_t* cum, int B, int64_t pos, 
 }
 
 constexpr int JO_THREADS = 128;
+constexpr int WT_UN = 4;  // tokens of a thread whose scores are loaded at once
 
 // Joins the pieces of the heads that several CTAs share, and adds the
-// weights.  Blocks 0 .. grid-1 (times the unit's query heads): block c joins the unit in
-// which stretch c begins, if stretch c is that unit's second.  The blocks after
-// them share the line of (sequence, KV head, tile) for the weights.
+// weights.  The first `wblocks` blocks share the line of (sequence, KV head, tile) for
+// the weights.  The others, one per stretch c and query head of a unit, join the
+// unit in which stretch c begins, if stretch c is that unit's second.
 template <typename T, int D, int HT>
 __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_constant__ DecodeArgs a, int wblocks) {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -567,9 +576,8 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
     const int all = a.cum[a.B], total = all * units;
     if (total == 0) return;
     const int per = stretch(total, a.grid);
-    const int joins = a.grid * a.GS;
-    if ((int)blockIdx.x < joins) {
-        const int c = blockIdx.x / a.GS, hd = blockIdx.x - c * a.GS;
+    if ((int)blockIdx.x >= wblocks) {
+        const int x = blockIdx.x - wblocks, c = x / a.GS, hd = x - c * a.GS;
         const int64_t pos = (int64_t)c * per;
         if (c == 0 || pos >= total) return;
         const int b = find_seq(a.cum, a.B, pos, units);
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         return;
     }
     // weights: an equal stretch of (sequence, KV head, tile) for every block
-    const int wb = blockIdx.x - joins;
+    const int wb = blockIdx.x;
     const int64_t wtotal = (int64_t)all * a.Hkv;
     const int64_t wper = (wtotal + wblocks - 1) / wblocks;
     int64_t pos = wb * wper;
@@ -659,6 +667,7 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         const int h = (int)((pos - base) / T_b), t0 = (int)(pos - base - (int64_t)h * T_b);
         const int n = (int)min((int64_t)(T_b - t0), end - pos);
         // log-sum-exp of the KV head's query heads, a warp each
+        int bad_any = 0;
         __syncthreads();
         for (int g = warp; g < a.G; g += JO_THREADS / 32) {
             const int k = g / HT, hd = g - k * HT, first = a.cum[b] * units + (h * a.NG + k) * T_b;
@@ -687,29 +696,51 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
                 for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 x = bad != 0.f ? INFINITY : sum == 0.f ? -INFINITY : M + log2f(sum);
             }
-            if (lane == 0) s_lse[g] = x;
+            bad_any |= x == INFINITY;
+            // a head without a finite score gets no weight: exp2(s - inf) = 0
+            if (lane == 0) s_lse[g] = x == -INFINITY ? INFINITY : x;
         }
-        __syncthreads();
         const int L = a.lens[b];
         float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
-        bool skip = false;
-        for (int g = 0; g < a.G; ++g) skip |= s_lse[g] == INFINITY;
-        if (!skip)
-            for (int x = tid; x < n * TILE; x += JO_THREADS) {
-                const int t = t0 * TILE + x;
-                if (t >= L) break;
-                float sum = 0.f;
-                for (int k = 0; k < a.NG; ++k) {
-                    const size_t tile = (size_t)a.cum[b] * units + (size_t)(h * a.NG + k) * T_b;
-                    const float* sc = a.scores + (tile * TILE + t) * a.GS;
-                    const int heads = min(HT, a.G - k * HT);
-                    for (int g = 0; g < heads; ++g) {
-                        const float lse = s_lse[k * HT + g];
-                        sum += lse == -INFINITY ? 0.f : ex2(sc[g] - lse);
+        auto weight_of = [&](int t) {
+            float sum = 0.f;
+            for (int k = 0; k < a.NG; ++k) {
+                const size_t tile = (size_t)a.cum[b] * units + (size_t)(h * a.NG + k) * T_b;
+                const float* sc = a.scores + (tile * TILE + t) * a.GS;
+                const float* lse = s_lse + k * HT;
+                const int heads = min(HT, a.G - k * HT);
+                if (a.GS % 4 == 0) {
+                    for (int g = 0; g < heads; g += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(sc + g);
+                        sum += ex2(y.x - lse[g]);
+                        if (g + 1 < heads) sum += ex2(y.y - lse[g + 1]);
+                        if (g + 2 < heads) sum += ex2(y.z - lse[g + 2]);
+                        if (g + 3 < heads) sum += ex2(y.w - lse[g + 3]);
+                    }
+                } else {
+                    for (int g = 0; g < heads; ++g) sum += ex2(sc[g] - lse[g]);
+                }
+            }
+            return sum;
+        };
+        if (!__syncthreads_or(bad_any)) {
+            const int t1 = min(L, (t0 + n) * TILE);
+            for (int x = t0 * TILE + tid; x < t1; x += WT_UN * JO_THREADS) {
+                float sum[WT_UN], old[WT_UN];
+#pragma unroll
+                for (int e = 0; e < WT_UN; ++e) {
+                    const int t = x + e * JO_THREADS;
+                    sum[e] = old[e] = 0.f;
+                    if (t < t1) {
+                        old[e] = w[t];
+                        sum[e] = weight_of(t);
                     }
                 }
-                w[t] += sum;
+#pragma unroll
+                for (int e = 0; e < WT_UN; ++e)
+                    if (x + e * JO_THREADS < t1) w[x + e * JO_THREADS] = old[e] + sum[e];
             }
+        }
         pos += n;
         while (pos < end && pos >= (int64_t)a.cum[b + 1] * a.Hkv) ++b;
     }
@@ -726,7 +757,7 @@ cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
     if (e != cudaSuccess || (p.grid == 1 && !a.weights)) return e;
     const int wblocks = a.weights ? 4 * p.grid : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid * a.GS + wblocks);
+    cfg.gridDim = dim3(wblocks + p.grid * a.GS);
     cfg.blockDim = dim3(JO_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
