@@ -34,6 +34,7 @@ constexpr int TILE = 16;              // tokens per step of a warp
 constexpr int STAGES = 3;             // ring depth of a warp, in tiles
 constexpr int MIN_TILES = 8;          // a CTA's shortest stretch
 constexpr float LN2 = 0.6931471805599453f;
+constexpr float SLACK = 8.f;          // log2: how far a score may pass the reference of the exponentials
 constexpr float BAD_SUM = -1.f;       // sum of a piece whose block table is out of range
 
 template <typename T, int D> struct Shape {
@@ -69,14 +70,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
 template <typename T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {
     static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
@@ -91,7 +92,7 @@ template <> struct Mma<__nv_bfloat16> {
 };
 template <> struct Mma<__half> {
     static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
     __shared__ __align__(16) float s_p[MMA ? 1 : NW][MMA ? 1 : TILE * HT];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int units = a.Hkv * a.NG;
+    const bool one_block = a.c.block_size % TILE == 0;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences without a token, and those whose length is out of range
@@ -236,9 +238,29 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             }
             return (int64_t)id * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
         };
-        auto issue = [&](int slot, int64_t off) {
+        // A lane copies piece `lane % CH` (or so) of every (32 / CH)-th row.  When the block size is a
+        // multiple of 16 a tile lies in one block, so its rows are token_stride apart; else
+        // every row has its own place.
+        auto issue = [&](int slot, int i, int64_t off) {
             const uint32_t dst = ring_a + slot * S::STAGE;
             static_assert(TILE * S::CH % 32 == 0, "a tile is whole warps of pieces");
+            if (one_block && 32 % S::CH == 0) {
+                constexpr int RS = 32 / S::CH ? 32 / S::CH : 1;  // rows of one step
+                const int row = lane / S::CH, ch = lane % S::CH;
+                const int64_t o = __shfl_sync(0xffffffffu, off, 0);  // of the tile's first token, or -1
+                const int left = o < 0 ? 0 : L - (t0 + i) * TILE - row;
+                int64_t at = (o < 0 ? 0 : o + row * a.c.token_stride) + ch * 16;
+                const int64_t step = o < 0 ? 0 : RS * a.c.token_stride;
+                const uint32_t d = dst + row * S::ROW + ch * 16;
+#pragma unroll
+                for (int j = 0; j < TILE / RS; ++j) {
+                    const int bytes = j * RS < left ? 16 : 0;  // rows past the sequence are zeros
+                    cp_async16(d + j * RS * S::ROW, kb + at, bytes);
+                    cp_async16(d + (TILE + j * RS) * S::ROW, vb + at, bytes);
+                    at += step;  // stays in the block
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < TILE * S::CH / 32; ++j) {
                 const int x = j * 32 + lane, row = x / S::CH, ch = x - row * S::CH;
@@ -252,7 +274,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
         int nxt = warp;  // next tile to request
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
-            if (nxt < n) issue(s, offset_of(nxt));
+            if (nxt < n) issue(s, nxt, offset_of(nxt));
             cp_commit();
             nxt += NW;
         }
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             {  // the slot that the previous step read is free
                 int free_slot = slot + STAGES - 1;
                 if (free_slot >= STAGES) free_slot -= STAGES;
-                if (nxt < n) issue(free_slot, off_next);
+                if (nxt < n) issue(free_slot, nxt, off_next);
                 cp_commit();
                 nxt += NW;
                 off_next = offset_of(nxt);
@@ -308,52 +330,70 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             const int tok = (t0 + i) * TILE;
             float* sc = a.weights ? a.scores + ((size_t)(pos + i) * TILE) * a.GS : nullptr;
             if constexpr (MMA) {
-                float c[NT][4];
+                float c[NT][4], c2[NT][4];  // two chains of products
 #pragma unroll
-                for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[j][e] = c2[j][e] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
                     uint32_t f[4];
                     ldsm4(f, kt + (lane % 16) * S::ROW + (kk * 2 + lane / 16) * 16);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) Mma<T>::run(c[j], f, qf[j][kk][0], qf[j][kk][1]);
+                    for (int j = 0; j < NT; ++j) Mma<T>::run(kk & 1 ? c2[j] : c[j], f, qf[j][kk][0], qf[j][kk][1]);
                 }
                 const int r0 = lane / 4;
                 const bool in0 = tok + r0 < L, in1 = tok + r0 + 8 < L;
-                uint32_t ph[NT][2], pl[NT][2];
-                float corr[NM];
                 bool grew = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        c[j][e] = in0 ? c[j][e] * a.scale_log2 : -INFINITY;
-                        c[j][2 + e] = in1 ? c[j][2 + e] * a.scale_log2 : -INFINITY;
+                        c[j][e] = in0 ? (c[j][e] + c2[j][e]) * a.scale_log2 : -INFINITY;
+                        c[j][2 + e] = in1 ? (c[j][2 + e] + c2[j][2 + e]) * a.scale_log2 : -INFINITY;
+                        grew |= fmaxf(c[j][e], c[j][2 + e]) > m[2 * j + e] + SLACK;
                     }
-                    const int hd0 = j * 8 + (lane % 4) * 2;
-                    if (sc && !(a.GS & 1) && hd0 < heads) {  // then an even number of heads, and pairs are aligned
-                        if (in0) *reinterpret_cast<float2*>(sc + r0 * a.GS + hd0) = make_float2(c[j][0], c[j][1]);
-                        if (in1) *reinterpret_cast<float2*>(sc + (r0 + 8) * a.GS + hd0) = make_float2(c[j][2], c[j][3]);
-                    }
+                    const int hd = j * 8 + (lane % 4) * 2;
+                    if (sc) {
+                        if (!(a.GS & 1)) {  // then `heads` is even too, and pairs are aligned
+                            if (in0 && hd < heads) *reinterpret_cast<float2*>(sc + r0 * a.GS + hd) = make_float2(c[j][0], c[j][1]);
+                            if (in1 && hd < heads)
+                                *reinterpret_cast<float2*>(sc + (r0 + 8) * a.GS + hd) = make_float2(c[j][2], c[j][3]);
+                        } else {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int hd = hd0 + e;
-                        if (sc && (a.GS & 1) && hd < heads) {
-                            if (in0) sc[r0 * a.GS + hd] = c[j][e];
-                            if (in1) sc[(r0 + 8) * a.GS + hd] = c[j][2 + e];
+                            for (int e = 0; e < 2; ++e) {
+                                if (in0 && hd + e < heads) sc[r0 * a.GS + hd + e] = c[j][e];
+                                if (in1 && hd + e < heads) sc[(r0 + 8) * a.GS + hd + e] = c[j][2 + e];
+                            }
                         }
-                        float x = fmaxf(c[j][e], c[j][2 + e]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int k = 0; k < NM; ++k) {
+                        const int j = k / 2, e = k % 2;
+                        float x = fmaxf(m[k], fmaxf(c[j][e], c[j][2 + e]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        const int k = 2 * j + e;
-                        const float mn = fmaxf(m[k], x);
-                        const float mu = mn == -INFINITY ? 0.f : mn;
-                        corr[k] = ex2(m[k] - mu);
-                        grew |= mn != m[k];
-                        m[k] = mn;
+                        const float corr = x == -INFINITY ? 1.f : ex2(m[k] - x);
+                        m[k] = x;
+                        l[k] *= corr;
+#pragma unroll
+                        for (int d = 0; d < KS; ++d) {
+                            o[j * KS + d][e] *= corr;
+                            o[j * KS + d][2 + e] *= corr;
+                        }
+                    }
+                }
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mu = m[2 * j + e] == -INFINITY ? 0.f : m[2 * j + e];
                         c[j][e] = ex2(c[j][e] - mu);
                         c[j][2 + e] = ex2(c[j][2 + e] - mu);
-                        l[k] = l[k] * corr[k] + (c[j][e] + c[j][2 + e]);
+                        l[2 * j + e] += c[j][e] + c[j][2 + e];
                     }
                     Mma<T>::split(c[j][0], c[j][1], ph[j][0], pl[j][0]);
                     Mma<T>::split(c[j][2], c[j][3], ph[j][1], pl[j][1]);
@@ -361,16 +401,6 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     for (int e = 0; e < 2; ++e) {
                         ph[j][e] = movm(ph[j][e]);
                         pl[j][e] = movm(pl[j][e]);
-                    }
-                }
-                if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                    for (int x = 0; x < NT * KS; ++x) {
-                        const int j = x / KS;
-                        o[x][0] *= corr[2 * j];
-                        o[x][1] *= corr[2 * j + 1];
-                        o[x][2] *= corr[2 * j];
-                        o[x][3] *= corr[2 * j + 1];
                     }
                 }
 #pragma unroll
@@ -547,12 +577,12 @@ __device__ __forceinline__ Pieces pieces_of(int first, int tiles, int per) {
     return p;
 }
 
-// The sequence that holds tile-per-unit `x` of the cumulative counts (the last b with cum[b] <= x).
-__device__ __forceinline__ int find_seq(const int32_t* cum, int B, int64_t pos, int units) {
+// The sequence that holds tile `pos` of the line (the last b whose tiles begin at or before it).
+__device__ __forceinline__ int find_seq(const int32_t* cum, int B, int pos, int units) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((int64_t)cum[mid] * units <= pos) lo = mid;
+        if (cum[mid] * units <= pos) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -563,27 +593,40 @@ constexpr int WT_UN = 4;  // tokens of a thread whose scores are loaded at once
 
 // Joins the pieces of the heads that several CTAs share, and adds the
 // weights.  The first `wblocks` blocks share the line of (sequence, KV head, tile) for
-// the weights.  The others, one per stretch c and query head of a unit, join the
-// unit in which stretch c begins, if stretch c is that unit's second.
+// the weights.  The others are one per query head of a unit: by_unit, of every unit;
+// else (more units than stretches) of the unit in which stretch y begins, if
+// that stretch is the unit's second.
 template <typename T, int D, int HT>
-__global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_constant__ DecodeArgs a, int wblocks) {
+__global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_constant__ DecodeArgs a, int wblocks,
+                                                                bool by_unit) {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int units = a.Hkv * a.NG;
     __shared__ float s_red[2][JO_THREADS / 32];
     __shared__ float4 s_o[JO_THREADS];
-    __shared__ float s_lse[128];
+    __shared__ __align__(16) float s_lse[128];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int all = a.cum[a.B], total = all * units;
     if (total == 0) return;
     const int per = stretch(total, a.grid);
     if ((int)blockIdx.x >= wblocks) {
-        const int x = blockIdx.x - wblocks, c = x / a.GS, hd = x - c * a.GS;
-        const int64_t pos = (int64_t)c * per;
-        if (c == 0 || pos >= total) return;
-        const int b = find_seq(a.cum, a.B, pos, units);
-        const int T_b = a.cum[b + 1] - a.cum[b], base = a.cum[b] * units;
-        const int u = ((int)pos - base) / T_b, first = base + u * T_b;
-        if (pos == first || pos - per > first) return;  // the unit's first stretch, or a later one than its second
+        const int x = blockIdx.x - wblocks, y = x / a.GS, hd = x - y * a.GS;
+        int b, u, T_b, first;
+        if (by_unit) {
+            b = y / units;
+            u = y - b * units;
+            T_b = a.cum[b + 1] - a.cum[b];
+            first = a.cum[b] * units + u * T_b;
+            if (T_b == 0 || first / per == (first + T_b - 1) / per) return;  // empty, or one stretch had it whole
+        } else {
+            if (y == 0 || (int64_t)y * per >= total) return;
+            const int pos = y * per;
+            b = find_seq(a.cum, a.B, pos, units);
+            const int base = a.cum[b] * units;
+            T_b = a.cum[b + 1] - a.cum[b];
+            u = (pos - base) / T_b;
+            first = base + u * T_b;
+            if (pos == first || pos - per > first) return;  // the unit's first stretch, or a later one than its second
+        }
         const int h = u / a.NG, g0 = (u - h * a.NG) * HT;
         if (g0 + hd >= a.G) return;
         const Pieces p = pieces_of(first, T_b, per);
@@ -655,17 +698,15 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
     }
     // weights: an equal stretch of (sequence, KV head, tile) for every block
     const int wb = blockIdx.x;
-    const int64_t wtotal = (int64_t)all * a.Hkv;
-    const int64_t wper = (wtotal + wblocks - 1) / wblocks;
-    int64_t pos = wb * wper;
-    const int64_t end = min(wtotal, pos + wper);
-    if (pos >= end) return;
+    const int wtotal = all * a.Hkv, wper = (wtotal + wblocks - 1) / wblocks;
+    if ((int64_t)wb * wper >= wtotal) return;
+    int pos = wb * wper;
+    const int end = min(wtotal, pos + wper);
     int b = find_seq(a.cum, a.B, pos, a.Hkv);
     while (pos < end) {
         const int T_b = a.cum[b + 1] - a.cum[b];
-        const int64_t base = (int64_t)a.cum[b] * a.Hkv;
-        const int h = (int)((pos - base) / T_b), t0 = (int)(pos - base - (int64_t)h * T_b);
-        const int n = (int)min((int64_t)(T_b - t0), end - pos);
+        const int base = a.cum[b] * a.Hkv, h = (pos - base) / T_b, t0 = pos - base - h * T_b;
+        const int n = min(T_b - t0, end - pos);
         // log-sum-exp of the KV head's query heads, a warp each
         int bad_any = 0;
         __syncthreads();
@@ -702,20 +743,26 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         }
         const int L = a.lens[b];
         float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
+        // scores of a token lie side by side: GS for each of the KV head's NG units
+        const float* scores = a.scores + ((size_t)a.cum[b] * units + (size_t)h * a.NG * T_b) * TILE * a.GS;
+        const size_t unit_scores = (size_t)T_b * TILE * a.GS;
         auto weight_of = [&](int t) {
             float sum = 0.f;
             for (int k = 0; k < a.NG; ++k) {
-                const size_t tile = (size_t)a.cum[b] * units + (size_t)(h * a.NG + k) * T_b;
-                const float* sc = a.scores + (tile * TILE + t) * a.GS;
+                const float* sc = scores + k * unit_scores + (size_t)t * a.GS;
                 const float* lse = s_lse + k * HT;
                 const int heads = min(HT, a.G - k * HT);
                 if (a.GS % 4 == 0) {
-                    for (int g = 0; g < heads; g += 4) {
-                        const float4 y = *reinterpret_cast<const float4*>(sc + g);
-                        sum += ex2(y.x - lse[g]);
-                        if (g + 1 < heads) sum += ex2(y.y - lse[g + 1]);
-                        if (g + 2 < heads) sum += ex2(y.z - lse[g + 2]);
-                        if (g + 3 < heads) sum += ex2(y.w - lse[g + 3]);
+#pragma unroll
+                    for (int g = 0; g < HT; g += 4) {
+                        if (g + 4 <= heads) {
+                            const float4 y = *reinterpret_cast<const float4*>(sc + g);
+                            const float4 z = *reinterpret_cast<const float4*>(lse + g);
+                            sum += (ex2(y.x - z.x) + ex2(y.y - z.y)) + (ex2(y.z - z.z) + ex2(y.w - z.w));
+                        } else {
+                            for (int e = g; e < heads; ++e) sum += ex2(sc[e] - lse[e]);
+                            break;
+                        }
                     }
                 } else {
                     for (int g = 0; g < heads; ++g) sum += ex2(sc[g] - lse[g]);
@@ -742,7 +789,7 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
             }
         }
         pos += n;
-        while (pos < end && pos >= (int64_t)a.cum[b + 1] * a.Hkv) ++b;
+        while (pos < end && pos >= a.cum[b + 1] * a.Hkv) ++b;
     }
 }
 
@@ -757,7 +804,9 @@ cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
     if (e != cudaSuccess || (p.grid == 1 && !a.weights)) return e;
     const int wblocks = a.weights ? 4 * p.grid : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(wblocks + p.grid * a.GS);
+    const int64_t all_units = (int64_t)a.B * a.Hkv * a.NG;
+    const bool by_unit = all_units <= p.grid;
+    cfg.gridDim = dim3(wblocks + (by_unit ? (int)all_units : p.grid) * a.GS);
     cfg.blockDim = dim3(JO_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -765,7 +814,7 @@ cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, HT>, a, wblocks);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, HT>, a, wblocks, by_unit);
 }
 
 template <typename T, int HT>
