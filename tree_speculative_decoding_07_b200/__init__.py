@@ -676,11 +676,11 @@ def _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_
     else:
         _want("out", out, q.dtype, (B, Hq, D))
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
     else:
         _want("lse", lse, torch.float32, (B, Hq))
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = kv_lens.new_empty(ws_bytes // 4)  # a multiple of 256
     else:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
@@ -722,7 +722,7 @@ def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, r
         _want("dst_block_table", dst_block_table, torch.int32, block_table.shape)
     ref = _cache_call(*fields, 0, weights.shape[-1])[1]
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+        kept = kv_lens.new_empty((B, Hkv, max(budget, 0)))
     else:
         _want("kept", kept, torch.int32, (B, Hkv, budget))
     if new_kv_lens is None:
@@ -816,7 +816,7 @@ def _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, 
     if q_out is not None:
         _want("q_out", q_out, k.dtype, (B, N, Hq, D))
     elif q is not None:
-        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        q_out = q.new_empty((B, N, Hq, D))
     s = lib().tv_rotary_write(ref, rot_ref, _addr(q), k.data_ptr(), v.data_ptr(), inv_freq.data_ptr(),
                               _addr(parent_idx), _addr(positions), _addr(position_base), prefix_lens.data_ptr(),
                               block_table.data_ptr(), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),

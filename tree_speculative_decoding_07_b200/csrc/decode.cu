@@ -34,7 +34,9 @@ constexpr int TILE = 16;              // tokens per step of a warp
 constexpr int STAGES = 3;             // ring depth of a warp, in tiles
 constexpr int MIN_TILES = 8;          // a CTA's shortest stretch
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float SLACK = 8.f;          // log2: how far a score may pass the reference of the exponentials
+// 16-bit path: the exponentials' reference lies 2^7 below the largest score it was set by, and
+// moves when a score passes it by more than 2^15.
+constexpr float REF_BELOW = 7.f, REF_MOVES = 15.f;
 constexpr float BAD_SUM = -1.f;       // sum of a piece whose block table is out of range
 
 template <typename T, int D> struct Shape {
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     for (int e = 0; e < 2; ++e) {
                         c[j][e] = in0 ? (c[j][e] + c2[j][e]) * a.scale_log2 : -INFINITY;
                         c[j][2 + e] = in1 ? (c[j][2 + e] + c2[j][2 + e]) * a.scale_log2 : -INFINITY;
-                        grew |= fmaxf(c[j][e], c[j][2 + e]) > m[2 * j + e] + SLACK;
+                        grew |= fmaxf(c[j][e], c[j][2 + e]) > m[2 * j + e] + REF_MOVES;
                     }
                     const int hd = j * 8 + (lane % 4) * 2;
                     if (sc) {
@@ -372,9 +374,10 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < NM; ++k) {
                         const int j = k / 2, e = k % 2;
-                        float x = fmaxf(m[k], fmaxf(c[j][e], c[j][2 + e]));
+                        float x = fmaxf(c[j][e], c[j][2 + e]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        x = fmaxf(m[k], x - REF_BELOW);
                         const float corr = x == -INFINITY ? 1.f : ex2(m[k] - x);
                         m[k] = x;
                         l[k] *= corr;
