@@ -54,7 +54,7 @@ SHORT = [0, 1, 15, 16, 17, 100, 0, 33]
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("d", [64, 96, 128, 256])
-@pytest.mark.parametrize("hkv,g", [(2, 1), (1, 3), (2, 4), (1, 7), (2, 8), (1, 12), (2, 16), (1, 40)])
+@pytest.mark.parametrize("hkv,g", [(2, 1), (1, 3), (2, 4), (1, 7), (2, 8), (1, 11), (1, 12), (2, 16), (1, 40)])
 def test_types_heads_and_short_lengths(dtype, d, hkv, g):
     _check(Cache(d + g, SHORT, hkv, d, dtype), hkv * g)
 
@@ -70,6 +70,15 @@ def test_block_sizes(dtype, block):
 @pytest.mark.parametrize("lens,hkv", [([5000], 1), ([3000, 1, 0, 777, 2048], 2), ([1, 9000], 1), ([20000], 2)])
 def test_heads_shared_by_many_ctas(dtype, g, lens, hkv):
     _check(Cache(len(lens), lens, hkv, 128, dtype), hkv * g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,g", [(128, 4), (256, 11), (64, 40), (96, 3)])
+@pytest.mark.parametrize("lens,hkv", [([600, 3], 1), ([640], 8), ([500] * 20, 4), ([2000] * 4, 8), ([1100], 2),
+                                      ([90, 2000, 17, 0, 2000], 4)])
+def test_both_ways_of_sharing_the_work(dtype, d, g, lens, hkv):
+    # short or many units by clusters, others by equal stretches; on either side of the borders
+    _check(Cache(d, lens, hkv, d, dtype), hkv * g)
 
 
 @pytest.mark.parametrize("weights", [False, True])
@@ -341,7 +350,7 @@ def test_wrapper_refusals():
         (dict(attn_weights=w.half()), TypeError), (dict(attn_weights=w[:, :1]), ValueError),
         (dict(attn_weights=w[:, :, :17].contiguous()), tv.TreeVerifyError), (dict(attn_weights=w[:, :, ::2]), ValueError),
         (dict(out=q), tv.TreeVerifyError), (dict(out=q.float()), TypeError),
-        (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), tv.TreeVerifyError),
+        (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"), attn_weights=w), tv.TreeVerifyError),
         (dict(max_kv_len=10 ** 6), tv.TreeVerifyError), (dict(softmax_scale=-1.0), tv.TreeVerifyError),
     ]
     for kw, error in bad:

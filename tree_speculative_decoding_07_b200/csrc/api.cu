@@ -203,9 +203,14 @@ tv_status decode_layout(const tv_cache_desc* d, bool weights, DecodeLayout* y) {
     if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128 && d->head_dim != 256) return TV_ERR_UNSUPPORTED;
     const int G = d->num_q_heads / d->num_kv_heads, max_len = cache_max_len(d);
     tv::DecodePlan& p = y->plan;
-    tv::decode_plan(d->dtype, d->batch, d->num_kv_heads, G, d->head_dim, max_len, device_sms(), &p);
+    tv::decode_plan(d->dtype, d->batch, d->num_kv_heads, G, d->head_dim, max_len, weights, device_sms(), &p);
     const int64_t tiles = (int64_t)d->batch * d->num_kv_heads * p.NG * ((max_len + 15) / 16);
     if (tiles > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
+    if (p.cluster) {  // the scores alone (and never nothing, so that a caller always has a workspace)
+        y->lse2 = y->ml = y->o = y->scores = 0;
+        y->bytes = weights ? align256(sizeof(float) * (size_t)tiles * 16 * p.GS) : 256;
+        return TV_OK;
+    }
     y->lse2 = align256(sizeof(int32_t) * ((size_t)d->batch + 1));
     y->ml = y->lse2 + (weights ? align256(sizeof(float) * (size_t)d->batch * d->num_q_heads) : 0);
     y->o = y->ml + align256(sizeof(float) * 2 * 2 * (size_t)p.grid * p.HT);
@@ -477,7 +482,7 @@ tv_status tv_decode_attention_plan(const tv_cache_desc* desc, int32_t with_weigh
     if (!plan) return TV_ERR_INVALID_ARG;
     plan->grid_ctas = y.plan.grid;
     plan->heads_per_unit = y.plan.HT;
-    plan->launches = y.plan.grid > 1 || with_weights ? 2 : 1;
+    plan->launches = y.plan.cluster ? 1 : 2;
     plan->smem_bytes = y.plan.smem;
     plan->workspace_bytes = y.bytes;
     return TV_OK;
@@ -513,6 +518,7 @@ tv_status tv_decode_attention(const tv_cache_desc* desc, const void* q, const vo
     a.B = desc->batch; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = a.Hq / a.Hkv;
     a.D = desc->head_dim; a.HT = y.plan.HT; a.GS = y.plan.GS; a.NG = y.plan.NG; a.grid = y.plan.grid;
     a.max_len = cache_max_len(desc);
+    a.cap_tiles = (a.max_len + 15) / 16;
     const float scale = desc->softmax_scale > 0.f ? desc->softmax_scale : 1.0f / sqrtf((float)desc->head_dim);
     a.scale_log2 = scale * 1.4426950408889634f;
     return tv::launch_decode(a, desc->dtype, y.plan, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TV_OK

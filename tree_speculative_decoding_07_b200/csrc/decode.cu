@@ -24,8 +24,12 @@
 // of K and V bound this kernel, not the matrix units.  fp32 runs on the CUDA
 // cores (two lanes per token for the scores, lanes over the head's dimensions
 // for the values).
+#include <cooperative_groups.h>
+
 #include "kernels.h"
 #include "tv_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace tv {
 namespace {
@@ -173,7 +177,9 @@ __device__ __forceinline__ int stretch(int total, int grid) {
     return per < MIN_TILES ? MIN_TILES : per;
 }
 
-template <typename T, int D, int HT>
+// CLUSTERS: a unit's tiles are shared by the CTAs of one cluster, which join their parts
+// through each other's shared memory and add the weights themselves: one launch.
+template <typename T, int D, int HT, bool CLUSTERS>
 __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using S = Shape<T, D>;
     constexpr int NW = S::NW, DE_THREADS = NW * 32;
@@ -185,40 +191,69 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
     __shared__ Start s_start;
     __shared__ int s_scan[NW];
     __shared__ float s_m[NW][HT], s_l[NW][HT];
+    __shared__ float2 s_ml[CLUSTERS ? HT : 1];
+    __shared__ float s_lse[CLUSTERS ? HT : 1];
     __shared__ __align__(16) float s_q[MMA ? 1 : HT * D];
     __shared__ __align__(16) float s_p[MMA ? 1 : NW][MMA ? 1 : TILE * HT];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int units = a.Hkv * a.NG;
-    const bool one_block = a.c.block_size % TILE == 0;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // sequences without a token, and those whose length is out of range
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int L = a.lens[b];
-        if (L > 0 && L <= a.max_len) continue;
-        if (L != 0 && tid == 0) report(a.status, TV_ERR_INVALID_ARG);
-        T* out = static_cast<T*>(a.out) + (size_t)b * a.Hq * D;
-        const float fill = L == 0 ? 0.f : __int_as_float(0x7fc00000);
-        for (int i = tid; i < a.Hq * D; i += DE_THREADS) Elem<T>::store(out + i, fill);
-        if (a.lse)
-            for (int i = tid; i < a.Hq; i += DE_THREADS)
-                a.lse[(size_t)b * a.Hq + i] = L == 0 ? -__int_as_float(0x7f800000) : fill;
+    int pos = 0, begin = 0, end = 1, b, u, t0, T_b, cum = 0, C = 1, rank = 0;
+    if constexpr (CLUSTERS) {
+        C = (int)cg::this_cluster().num_blocks();
+        rank = (int)cg::this_cluster().block_rank();
+        const int unit = blockIdx.x / C;
+        b = unit / units;
+        u = unit - b * units;
+        T_b = tiles_of(a, b);
+        if (T_b == 0) {  // no token, or a length out of range: the same in the whole cluster
+            const int L = a.lens[b], h = u / a.NG, g0 = (u - h * a.NG) * HT, heads = min(HT, a.G - g0);
+            const size_t at = (size_t)b * a.Hq + h * a.G + g0;
+            const float fill = L == 0 ? 0.f : __int_as_float(0x7fc00000);
+            if (rank == 0) {
+                if (L != 0 && tid == 0) report(a.status, TV_ERR_INVALID_ARG);
+                for (int i = tid; i < heads * D; i += DE_THREADS) Elem<T>::store(static_cast<T*>(a.out) + at * D + i, fill);
+                if (a.lse && tid < heads) a.lse[at + tid] = L == 0 ? -__int_as_float(0x7f800000) : fill;
+            }
+            return;
+        }
+        t0 = (int)((int64_t)T_b * rank / C);
+        pos = unit * a.cap_tiles + t0;  // where the scores go
+        end = pos + (int)((int64_t)T_b * (rank + 1) / C) - t0;
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        // sequences without a token, and those whose length is out of range
+        for (int x = blockIdx.x; x < a.B; x += gridDim.x) {
+            const int L = a.lens[x];
+            if (L > 0 && L <= a.max_len) continue;
+            if (L != 0 && tid == 0) report(a.status, TV_ERR_INVALID_ARG);
+            T* out = static_cast<T*>(a.out) + (size_t)x * a.Hq * D;
+            const float fill = L == 0 ? 0.f : __int_as_float(0x7fc00000);
+            for (int i = tid; i < a.Hq * D; i += DE_THREADS) Elem<T>::store(out + i, fill);
+            if (a.lse)
+                for (int i = tid; i < a.Hq; i += DE_THREADS)
+                    a.lse[(size_t)x * a.Hq + i] = L == 0 ? -__int_as_float(0x7f800000) : fill;
+        }
+        find_start<NW>(a, units,
+                       [&](int total) { return (int)min((int64_t)total, (int64_t)blockIdx.x * stretch(total, a.grid)); },
+                       blockIdx.x == 0, &s_start, s_scan);
+        const int total = s_start.total, per = stretch(total, a.grid);
+        const int64_t begin64 = (int64_t)blockIdx.x * per;
+        if (begin64 >= total) return;
+        begin = pos = (int)begin64;
+        end = (int)min((int64_t)total, begin64 + per);
+        b = s_start.b;
+        cum = s_start.cum;
+        T_b = tiles_of(a, b);
+        u = (pos - cum * units) / T_b;
+        t0 = (pos - cum * units) - u * T_b;
     }
-    find_start<NW>(a, units, [&](int total) { return (int)min((int64_t)total, (int64_t)blockIdx.x * stretch(total, a.grid)); },
-               blockIdx.x == 0, &s_start, s_scan);
-    const int total = s_start.total, per = stretch(total, a.grid);
-    const int64_t begin64 = (int64_t)blockIdx.x * per;
-    if (begin64 >= total) return;
-    const int begin = (int)begin64, end = (int)min((int64_t)total, begin64 + per);
-    int pos = begin, b = s_start.b, cum = s_start.cum;
-    int T_b = tiles_of(a, b);
-    int u = (pos - cum * units) / T_b, t0 = (pos - cum * units) - u * T_b;
 
     unsigned char* ring = ring_all + warp * S::RING;
     const uint32_t ring_a = smem_u32(ring);
 
-    while (pos < end) {
-        const int n = min(T_b - t0, end - pos);  // tiles of this piece
+    do {
+        const int n = min(T_b - t0, end - pos);  // tiles of this piece (none for a CTA that a short sequence leaves over)
         const int L = a.lens[b];
         const int h = u / a.NG, g0 = (u - h * a.NG) * HT;
         const int heads = min(HT, a.G - g0);     // query heads of this unit
@@ -240,29 +275,9 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             }
             return (int64_t)id * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
         };
-        // A lane copies piece `lane % CH` (or so) of every (32 / CH)-th row.  When the block size is a
-        // multiple of 16 a tile lies in one block, so its rows are token_stride apart; else
-        // every row has its own place.
-        auto issue = [&](int slot, int i, int64_t off) {
+        auto issue = [&](int slot, int64_t off) {
             const uint32_t dst = ring_a + slot * S::STAGE;
             static_assert(TILE * S::CH % 32 == 0, "a tile is whole warps of pieces");
-            if (one_block && 32 % S::CH == 0) {
-                constexpr int RS = 32 / S::CH ? 32 / S::CH : 1;  // rows of one step
-                const int row = lane / S::CH, ch = lane % S::CH;
-                const int64_t o = __shfl_sync(0xffffffffu, off, 0);  // of the tile's first token, or -1
-                const int left = o < 0 ? 0 : L - (t0 + i) * TILE - row;
-                int64_t at = (o < 0 ? 0 : o + row * a.c.token_stride) + ch * 16;
-                const int64_t step = o < 0 ? 0 : RS * a.c.token_stride;
-                const uint32_t d = dst + row * S::ROW + ch * 16;
-#pragma unroll
-                for (int j = 0; j < TILE / RS; ++j) {
-                    const int bytes = j * RS < left ? 16 : 0;  // rows past the sequence are zeros
-                    cp_async16(d + j * RS * S::ROW, kb + at, bytes);
-                    cp_async16(d + (TILE + j * RS) * S::ROW, vb + at, bytes);
-                    at += step;  // stays in the block
-                }
-                return;
-            }
 #pragma unroll
             for (int j = 0; j < TILE * S::CH / 32; ++j) {
                 const int x = j * 32 + lane, row = x / S::CH, ch = x - row * S::CH;
@@ -273,15 +288,10 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                 cp_async16(dst + TILE * S::ROW + row * S::ROW + ch * 16, vb + at, bytes);
             }
         };
-        int nxt = warp;  // next tile to request
+        // block ids of the first tiles and the queries: independent loads, all under way together
+        int64_t off[STAGES];
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) {
-            if (nxt < n) issue(s, nxt, offset_of(nxt));
-            cp_commit();
-            nxt += NW;
-        }
-        int64_t off_next = offset_of(nxt);
-
+        for (int e = 0; e < STAGES; ++e) off[e] = offset_of(warp + e * NW);
         // queries
         uint32_t qf[MMA ? NT : 1][MMA ? KS : 1][2];
         if constexpr (MMA) {
@@ -300,6 +310,15 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             for (int i = tid; i < HT * D; i += DE_THREADS) s_q[i] = i < heads * D ? reinterpret_cast<const float*>(q)[i] : 0.f;
             __syncthreads();
         }
+
+        int nxt = warp;  // next tile to request
+#pragma unroll
+        for (int e = 0; e < STAGES - 1; ++e) {
+            if (nxt < n) issue(e, off[e]);
+            cp_commit();
+            nxt += NW;
+        }
+        int64_t off_next = off[STAGES - 1];
 
         // running softmax: a lane of the matrix path has two heads per 8 (columns
         // 2 (lane % 4) and the next); on the fp32 path every lane has all HT
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             {  // the slot that the previous step read is free
                 int free_slot = slot + STAGES - 1;
                 if (free_slot >= STAGES) free_slot -= STAGES;
-                if (nxt < n) issue(free_slot, nxt, off_next);
+                if (nxt < n) issue(free_slot, off_next);
                 cp_commit();
                 nxt += NW;
                 off_next = offset_of(nxt);
@@ -357,7 +376,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     }
                     const int hd = j * 8 + (lane % 4) * 2;
                     if (sc) {
-                        if (!(a.GS & 1)) {  // then `heads` is even too, and pairs are aligned
+                        if (!(a.GS & 1)) {  // pairs are aligned; one may reach past `heads`, inside the GS of a token
                             if (in0 && hd < heads) *reinterpret_cast<float2*>(sc + r0 * a.GS + hd) = make_float2(c[j][0], c[j][1]);
                             if (in1 && hd < heads)
                                 *reinterpret_cast<float2*>(sc + (r0 + 8) * a.GS + hd) = make_float2(c[j][2], c[j][3]);
@@ -492,7 +511,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                 s_l[warp][hd] = l[k];
             }
         }
-        const bool any_bad = __syncthreads_or(bad) != 0;
+        int any_bad = __syncthreads_or(bad);
         constexpr int OROW = D + 4;
         static_assert(HT * OROW * 4 <= S::RING, "a warp's outputs fit its ring");
         float* so = reinterpret_cast<float*>(ring);
@@ -515,9 +534,11 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             }
         }
         __syncthreads();
-        const bool whole = n == T_b;
+        const bool whole = !CLUSTERS && n == T_b;
         const int part = 2 * blockIdx.x + (pos == begin ? 0 : 1);
         if (any_bad && tid == 0) report(a.status, TV_ERR_BLOCK_TABLE);
+        float* joint = reinterpret_cast<float*>(ring_all) + HT * OROW;  // clusters: this CTA's sums, behind warp 0's
+        static_assert(2 * HT * OROW * 4 <= S::RING, "a warp's outputs and the CTA's fit its ring");
         for (int x = tid; x < heads * (D / 4); x += DE_THREADS) {
             const int hd = x / (D / 4), d = (x - hd * (D / 4)) * 4;
             float M = s_m[0][hd], sum = 0.f;
@@ -549,10 +570,73 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     // +inf marks a head whose weights stay as they were
                     if (a.weights) a.lse2[at] = any_bad ? INFINITY : l2;
                 }
+            } else if constexpr (CLUSTERS) {
+                *reinterpret_cast<float4*>(joint + hd * OROW + d) = r;
+                if (d == 0) s_ml[hd] = make_float2(M, any_bad ? BAD_SUM : sum);
             } else {
                 *reinterpret_cast<float4*>(a.part_o + ((size_t)part * HT + hd) * D + d) = r;
                 if (d == 0) a.part_ml[(size_t)part * HT + hd] = make_float2(M, any_bad ? BAD_SUM : sum);
             }
+        }
+        if constexpr (CLUSTERS) {
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            const size_t at = (size_t)b * a.Hq + h * a.G + g0;
+            // every head's common reference, sum and flag, in rank order
+            if (tid < heads) {
+                float M = -INFINITY, sum = 0.f;
+                bool flag = false;
+                for (int c = 0; c < C; ++c) {
+                    const float2 ml = *cluster.map_shared_rank(&s_ml[tid], c);
+                    M = fmaxf(M, ml.x);
+                    flag |= ml.y == BAD_SUM;
+                }
+                for (int c = 0; c < C; ++c) {
+                    const float2 ml = *cluster.map_shared_rank(&s_ml[tid], c);
+                    sum += ml.y * ex2(ml.x - (M == -INFINITY ? 0.f : M));
+                }
+                const float l2 = sum == 0.f ? -INFINITY : M + log2f(sum), nan = __int_as_float(0x7fc00000);
+                s_m[0][tid] = M == -INFINITY ? 0.f : M;
+                s_l[0][tid] = flag ? nan : sum == 0.f ? 0.f : 1.f / sum;
+                // a head without a finite score gets no weight: exp2(s - inf) = 0
+                s_lse[tid] = l2 == -INFINITY ? INFINITY : l2;
+                if (a.lse && rank == 0) a.lse[at + tid] = flag ? nan : l2 * LN2;
+                any_bad = flag;
+            }
+            any_bad = __syncthreads_or(any_bad);
+            for (int x = rank * DE_THREADS + tid; x < heads * (D / 4); x += C * DE_THREADS) {
+                const int hd = x / (D / 4), d = (x - hd * (D / 4)) * 4;
+                const float mu = s_m[0][hd], inv = s_l[0][hd];
+                float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = 0; c < C; ++c) {
+                    const float f = ex2(cluster.map_shared_rank(&s_ml[hd], c)->x - mu);
+                    const float4 y = *reinterpret_cast<const float4*>(cluster.map_shared_rank(joint + hd * OROW + d, c));
+                    r.x += y.x * f;
+                    r.y += y.y * f;
+                    r.z += y.z * f;
+                    r.w += y.w * f;
+                }
+                T* out = static_cast<T*>(a.out) + (at + hd) * D + d;
+                Elem<T>::store(out, r.x * inv);
+                Elem<T>::store(out + 1, r.y * inv);
+                Elem<T>::store(out + 2, r.z * inv);
+                Elem<T>::store(out + 3, r.w * inv);
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read its peers' parts
+            if (a.weights && !any_bad) {  // one unit per KV head here; this CTA wrote these scores itself
+                float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
+                const float* scores = a.scores + (size_t)(pos - t0) * TILE * a.GS;
+                const int end_t = min(L, (t0 + n) * TILE);
+                for (int t = t0 * TILE + tid; t < end_t; t += DE_THREADS) {
+                    float sum = 0.f;
+                    for (int g = 0; g < heads; ++g) sum += ex2(scores[(size_t)t * a.GS + g] - s_lse[g]);
+                    w[t] += sum;
+                }
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // and they this CTA's
+            return;
         }
         __syncthreads();  // the rings and the shared values are free for the next piece
 
@@ -563,7 +647,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             cum += T_b;
             if (pos < end) do T_b = tiles_of(a, ++b); while (T_b == 0);
         }
-    }
+    } while (pos < end);
 }
 
 // Where a unit's tiles lie on the line and which stretches cover them.
@@ -798,13 +882,32 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
 
 template <typename T, int D, int HT>
 cudaError_t launch(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
-    auto kern = decode_kernel<T, D, HT>;
-    static SmemLimit limit;  // one size for every call of this kernel
-    cudaError_t e = limit.allow((const void*)kern, Shape<T, D>::NW * Shape<T, D>::RING);
+    constexpr int threads = Shape<T, D>::NW * 32, smem = Shape<T, D>::NW * Shape<T, D>::RING;
+    if (p.cluster) {
+        auto kern = decode_kernel<T, D, HT, true>;
+        static SmemLimit limit;  // one size for every call of this kernel
+        cudaError_t e = limit.allow((const void*)kern, smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(p.grid);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = p.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, a);
+    }
+    auto kern = decode_kernel<T, D, HT, false>;
+    static SmemLimit limit;
+    cudaError_t e = limit.allow((const void*)kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<p.grid, Shape<T, D>::NW * 32, Shape<T, D>::NW * Shape<T, D>::RING, st>>>(a);
+    kern<<<p.grid, threads, smem, st>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || (p.grid == 1 && !a.weights)) return e;
+    if (e != cudaSuccess) return e;
     const int wblocks = a.weights ? 4 * p.grid : 0;
     cudaLaunchConfig_t cfg = {};
     const int64_t all_units = (int64_t)a.B * a.Hkv * a.NG;
@@ -834,7 +937,7 @@ cudaError_t by_dim(const DecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
 
 }  // namespace
 
-void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, int sms, DecodePlan* p) {
+void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, bool weights, int sms, DecodePlan* p) {
     const int es = dtype == TV_F32 ? 4 : 2;
     if (dtype == TV_F32) p->HT = G <= 4 ? 4 : 8;
     else p->HT = G <= 8 || D > 128 ? 8 : 16;
@@ -846,7 +949,23 @@ void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, int sms, 
     int per_sm = (228 * 1024) / (p->smem + fixed);
     if (per_sm < 1) per_sm = 1;
     if (per_sm > 4) per_sm = 4;
-    const int64_t tiles = (int64_t)B * Hkv * p->NG * ((max_len + TILE - 1) / TILE);
+    const int64_t units = (int64_t)B * Hkv * p->NG, cap_tiles = (max_len + TILE - 1) / TILE, tiles = units * cap_tiles;
+    // Clusters of up to 8 CTAs per unit, down to 4 tiles (one per warp) for each, where that is short
+    // work (8 tiles per CTA; 1,024 tokens of one sequence with 8 KV heads: 6.7 us, by stretches 8.4) or
+    // fills most of the GPU (up to 32 tiles; 4 x 2,048 tokens 11.4 us against 14.6, 64 x 512 32.3
+    // against 34.1).  Past that the equal stretches win: they use every SM (one sequence of 4,096: 9.9
+    // against 11.8) and do not depend on how long each sequence of a batch is.  Clusters of 16 lost
+    // to 8 at 1,024 tokens (7.7 us).  Weights over several units of a KV head need the second kernel.
+    p->cluster = 0;
+    if (!weights || p->NG == 1) {
+        int c = 1;
+        while (c < 8 && c * 4 < cap_tiles && units * c * 2 <= (int64_t)per_sm * sms) c *= 2;
+        if (cap_tiles <= c * 8 || (cap_tiles <= c * 32 && units * c * 4 >= 3 * (int64_t)sms)) {
+            p->cluster = c;
+            p->grid = (int)(units * c);
+            return;
+        }
+    }
     int64_t grid = (tiles + MIN_TILES - 1) / MIN_TILES;
     if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
     if (grid < 1) grid = 1;

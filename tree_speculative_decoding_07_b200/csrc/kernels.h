@@ -163,13 +163,15 @@ struct DecodeArgs {
     float* part_o;         // [2 * grid][HT][D] their unnormalised outputs
     float* scores;         // [tile][16][GS] scaled scores, log2 domain (with weights)
     int B, Hq, Hkv, G, D, HT, GS, NG, max_len, grid;
+    int cap_tiles;         // 16-token tiles of max_len
     float scale_log2;
 };
 struct DecodePlan {
-    int HT, NG, GS, grid, smem;  // query heads per unit, units per KV head, heads of a full unit
+    int HT, NG, GS, grid, smem, cluster;  // query heads per unit, units per KV head, heads of a full unit;
+                                           // cluster: CTAs that share a unit (0: equal stretches)
 };
 // dtype: 0 bf16, 1 fp32, 2 fp16
-void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, int sms, DecodePlan* p);
+void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, bool weights, int sms, DecodePlan* p);
 cudaError_t launch_decode(const DecodeArgs& a, int dtype, const DecodePlan& p, cudaStream_t st);
 
 // Rotary positions: q and k rotated, k and v written into the cache.
