@@ -559,13 +559,16 @@ typedef struct {
  * [0, max_kv_len] or a block id out of range gives the sequence NaN rows, leaves
  * its attn_weights as they were and writes TV_ERR_INVALID_ARG or
  * TV_ERR_BLOCK_TABLE to *dev_status.  Cache slots past kv_lens[b] are not read.
- * Workspace: tv_decode_attention_workspace_size bytes, 256-byte aligned, with
- * the rules of tv_tree_attention's; it depends on the current device, and with
- * weights it holds 4 bytes for every (query head, position below max_kv_len).
+ * Workspace: tv_decode_attention_workspace_size bytes (0 when none: small calls
+ * without weights), 256-byte aligned, with the rules of tv_tree_attention's; it
+ * depends on the current device, and with weights it holds 4 bytes for every
+ * (query head, position below max_kv_len).
  * Alignment: q and out 16 bytes, q_stride a multiple of 16 bytes.
  */
 typedef struct {
-    int32_t grid_ctas;           /* CTAs that share the work of the batch equally, in 16-token tiles */
+    int32_t grid_ctas;           /* CTAs of the main launch */
+    int32_t cluster_ctas;        /* CTAs (one cluster) that share a KV head of a sequence; 0: all CTAs share
+                                    the batch's 16-token tiles equally, and a second launch joins */
     int32_t heads_per_unit;      /* query heads that one pass over a KV head's rows serves */
     int32_t launches;            /* kernel launches per call */
     int32_t smem_bytes;          /* dynamic shared memory per CTA */

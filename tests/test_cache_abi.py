@@ -82,13 +82,16 @@ def test_decode_refuses_bad_arguments():
     for name in ("q", "k", "v", "out"):
         assert _decode(d, **{name: A + 8}) == tv.TV_ERR_INVALID_ARG
     assert _decode(d, q=A, out=A) == tv.TV_ERR_INVALID_ARG
-    need = tv.tv_decode_attention_workspace_size(d)
-    assert need > 0 and need % 256 == 0
-    assert _decode(d, size=need - 1) == tv.TV_ERR_WORKSPACE
-    assert _decode(d, ws=None) == tv.TV_ERR_WORKSPACE
-    assert _decode(d, ws=A + 128) == tv.TV_ERR_WORKSPACE
-    assert tv.tv_decode_attention_workspace_size(d, True) > need
-    assert _decode(d, w=A, size=need) == tv.TV_ERR_WORKSPACE
+    # short work needs a workspace for the weights only, equal stretches always one
+    assert tv.tv_decode_attention_workspace_size(d) == 0
+    long = _desc(max_blocks_per_seq=900)
+    for x, w in ((d, A), (long, None), (long, A)):
+        need = tv.tv_decode_attention_workspace_size(x, w is not None)
+        assert need > 0 and need % 256 == 0
+        assert _decode(x, w=w, size=need - 1) == tv.TV_ERR_WORKSPACE
+        assert _decode(x, w=w, ws=None) == tv.TV_ERR_WORKSPACE
+        assert _decode(x, w=w, ws=A + 128) == tv.TV_ERR_WORKSPACE
+    assert tv.tv_decode_attention_workspace_size(long, True) > tv.tv_decode_attention_workspace_size(long)
     for dim in (16, 80, 192):
         assert _decode(_desc(head_dim=dim)) == tv.TV_ERR_UNSUPPORTED
     # more tiles than the line's 32-bit numbers hold
@@ -106,7 +109,9 @@ def test_decode_plans():
                 assert 1 <= p.smem_bytes <= 227 * 1024 and p.grid_ctas >= 1 and p.launches in (1, 2)
                 assert p.heads_per_unit in (4, 8, 16)
     small = tv.tv_decode_attention_plan(_desc(batch=1, max_kv_len=16), False)
-    assert small.grid_ctas == 2 or small.grid_ctas == 1
+    assert (small.grid_ctas, small.cluster_ctas, small.launches) == (2, 1, 1)
+    large = tv.tv_decode_attention_plan(_desc(batch=1, max_blocks_per_seq=9000), False)
+    assert large.cluster_ctas == 0 and large.launches == 2
     plan = tv.TvDecodePlan()
     assert tv.lib().tv_decode_attention_plan(ctypes.byref(_desc()), 0, None) == tv.TV_ERR_INVALID_ARG
     assert tv.lib().tv_decode_attention_plan(None, 0, ctypes.byref(plan)) == tv.TV_ERR_INVALID_ARG

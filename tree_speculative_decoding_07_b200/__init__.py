@@ -6,7 +6,9 @@ This module is a thin ctypes binding over the C ABI in
 arguments as the C calls (device pointers taken from torch tensors, the
 current torch CUDA stream unless another is given) and return the C status.
 All computation happens in the library's kernels; torch only provides
-device memory and streams.
+device memory and streams.  The wrappers of the calls on the cache marshal
+their arguments in C++ (``binding/marshal.cpp``), which is half of a small
+call's time.
 
 Convenience wrappers :func:`tree_attention` and :func:`verify_sample`
 allocate outputs/workspace with torch and raise on a non-OK status.
@@ -14,7 +16,6 @@ allocate outputs/workspace with torch and raise on a non-OK status.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -58,8 +59,8 @@ class TvCacheDesc(ctypes.Structure):
 
 
 class TvDecodePlan(ctypes.Structure):
-    _fields_ = [("grid_ctas", ctypes.c_int32), ("heads_per_unit", ctypes.c_int32), ("launches", ctypes.c_int32),
-                ("smem_bytes", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
+    _fields_ = [("grid_ctas", ctypes.c_int32), ("cluster_ctas", ctypes.c_int32), ("heads_per_unit", ctypes.c_int32),
+                ("launches", ctypes.c_int32), ("smem_bytes", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class TvRotaryDesc(ctypes.Structure):
@@ -528,40 +529,23 @@ def tv_rotary_write(desc, rot, q, k, v, inv_freq, parent_idx, positions, positio
                                      _stream(stream)))
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+_calls = None
 
 
-def _on_gpu(stream, first, others):
-    """The GPU that every tensor has to lie on, the stream to run on as an address, and the
-    context to enter for it (None: the call's GPU and stream are the current ones).  What is
-    allocated inside it belongs to the stream that the kernels run on."""
-    import torch
-    at = first.get_device()
-    if at < 0:
-        raise ValueError("all tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"all tensors must be on one GPU: {first.device} and {t.device}")
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(at)
-        return raw, None if torch._C._cuda_getDevice() == at else torch.cuda.device(at)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=first.device)
-    elif stream.device != first.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
-    return stream.cuda_stream, torch.cuda.stream(stream)  # makes its GPU current too
-
-
-def _want(name, t, dtype, shape):
-    """A contiguous tensor of the given type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+def _native():
+    """The marshalling module of the three calls below; raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        lib()
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise ImportError(f"_marshal.so not built in {_HERE} ({e}); run __graft_entry__.build() or python -m "
+                              "tree_speculative_decoding_07_b200.build_lib") from e
+        _marshal.set_error(TreeVerifyError)
+        _calls = _marshal
+    return _calls
 
 
 _cache_types: dict = {}
@@ -572,11 +556,6 @@ def cache_desc(k_cache, v_cache, block_table, num_q_heads: int | None = None, so
     """Descriptor of a paged cache from tensors: caches [nb][block][Hkv][D] of any
     strides with contiguous head rows (equal for K and V), block_table [B][max_blocks]
     int32."""
-    return TvCacheDesc(*_cache_fields(k_cache, v_cache, block_table, num_q_heads, softmax_scale, max_kv_len))
-
-
-def _cache_fields(k_cache, v_cache, block_table, num_q_heads, softmax_scale, max_kv_len):
-    """The values of the descriptor's fields up to head_stride."""
     import torch
     if not _cache_types:
         _cache_types.update({torch.bfloat16: TV_BF16, torch.float32: TV_F32, torch.float16: TV_F16})
@@ -594,8 +573,8 @@ def _cache_fields(k_cache, v_cache, block_table, num_q_heads, softmax_scale, max
         if _row_strides("v_cache", v_cache) != strides:
             raise ValueError("k_cache and v_cache must have the same strides")
     b, mb = block_table.shape
-    return (b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
-            int(max_kv_len), *strides)
+    return TvCacheDesc(b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
+                       int(max_kv_len), *strides, 0, 0)
 
 
 def _row_strides(name, c):
@@ -613,84 +592,18 @@ def _row_strides(name, c):
     return strides
 
 
-# Descriptors by the values of their fields: shared by calls and threads, never changed.
-
-@functools.lru_cache(maxsize=256)
-def _cache_call(*fields):
-    desc = TvCacheDesc(*fields)
-    return desc, ctypes.byref(desc)
-
-
-@functools.lru_cache(maxsize=256)
-def _rotary_call(*fields, axes=b""):
-    rot = TvRotaryDesc(*fields)
-    ctypes.memmove(rot.axis_of_pair, axes, len(axes))
-    return rot, ctypes.byref(rot)
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_call(gpu, with_weights, *fields):
-    """Descriptor and workspace size of a decode call of these sizes on this GPU (current)."""
-    desc = TvCacheDesc(*fields)
-    plan = tv_decode_attention_plan(desc, with_weights)
-    return desc, ctypes.byref(desc), plan.workspace_bytes
-
-
 def decode_attention(q, k_cache, v_cache, block_table, kv_lens, softmax_scale: float = 0.0, attn_weights=None,
                      out=None, lse=None, workspace=None, max_kv_len: int = 0, dev_status=None, stream=None):
     """Run tv_decode_attention: one new token per sequence, q [B][Hq][D] (sequences may lie
     apart), over the paged cache; returns (out, lse [B][Hq] float32).  attn_weights
     [B][Hkv][width] float32, width at least max_kv_len (default: the block table's
-    capacity), is added to in place."""
-    raw, ctx = _on_gpu(stream, q, (k_cache, v_cache, block_table, kv_lens, attn_weights, out, lse, workspace,
-                                   dev_status))
-    if ctx is not None:
-        with ctx:
-            return _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse,
-                           workspace, max_kv_len, dev_status)
-    return _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse, workspace,
-                   max_kv_len, dev_status)
+    capacity), is added to in place.
 
-
-def _decode(raw, q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse, workspace,
-            max_kv_len, dev_status):
-    import torch
-    if q.dim() != 3 or q.dtype != k_cache.dtype:
-        raise TypeError("q must be [batch][heads][head_dim] of the caches' type")
-    B, Hq, D = q.shape
-    fields = _cache_fields(k_cache, v_cache, block_table, Hq, softmax_scale, max_kv_len)
-    if fields[0] != B or fields[3] != D:
-        raise ValueError("q, block_table and the caches disagree on batch or head_dim")
-    q_stride = weight_stride = 0
-    if not q.is_contiguous():
-        if (D > 1 and q.stride(2) != 1) or (Hq > 1 and q.stride(1) != D):
-            raise ValueError("q: the heads of a sequence must be contiguous")
-        q_stride = q.stride(0) if B > 1 else 0
-    _want("kv_lens", kv_lens, torch.int32, (B,))
-    if attn_weights is not None:
-        weight_stride = attn_weights.shape[-1]
-        _want("attn_weights", attn_weights, torch.float32, (B, fields[2], weight_stride))
-    desc, ref, ws_bytes = _decode_call(q.get_device(), attn_weights is not None, *fields, q_stride, weight_stride)
-    if out is None:
-        out = torch.empty_like(q) if not q_stride else torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-    else:
-        _want("out", out, q.dtype, (B, Hq, D))
-    if lse is None:
-        lse = q.new_empty((B, Hq), dtype=torch.float32)
-    else:
-        _want("lse", lse, torch.float32, (B, Hq))
-    if workspace is None:
-        workspace = kv_lens.new_empty(ws_bytes // 4)  # a multiple of 256
-    else:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    s = lib().tv_decode_attention(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                  kv_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), _addr(attn_weights),
-                                  workspace.data_ptr(), ws_bytes, _addr(dev_status), raw)
-    if s != TV_OK:
-        raise TreeVerifyError(s, "tv_decode_attention")
-    return out, lse
+    This call and the two below check their tensors (types, shapes, strides, one GPU), run on
+    that GPU's current stream or on `stream` (a torch stream or an address), and allocate on
+    it what they are not given."""
+    return _native().decode_attention(q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out,
+                                      lse, workspace, max_kv_len, dev_status, stream)
 
 
 def evict_cache(k_cache, v_cache, block_table, kv_lens, weights, budget: int, sink: int = 0, recent: int = 0,
@@ -699,57 +612,8 @@ def evict_cache(k_cache, v_cache, block_table, kv_lens, weights, budget: int, si
     """Run tv_evict_cache on the caches (in place, or into the blocks of dst_block_table);
     returns (new_kv_lens [B], kept [B][Hkv][budget]), int32.  weights [B][Hkv][width]
     float32; weights_out, of its shape, may be weights itself."""
-    raw, ctx = _on_gpu(stream, k_cache, (v_cache, block_table, kv_lens, weights, dst_block_table, weights_out, kept,
-                                         new_kv_lens, dev_status))
-    if ctx is not None:
-        with ctx:
-            return _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table,
-                          weights_out, kept, new_kv_lens, max_kv_len, dev_status)
-    return _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table,
-                  weights_out, kept, new_kv_lens, max_kv_len, dev_status)
-
-
-def _evict(raw, k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent, dst_block_table, weights_out,
-           kept, new_kv_lens, max_kv_len, dev_status):
-    import torch
-    fields = _cache_fields(k_cache, v_cache, block_table, None, 0.0, max_kv_len)
-    B, Hkv, budget = fields[0], fields[2], int(budget)
-    _want("kv_lens", kv_lens, torch.int32, (B,))
-    _want("weights", weights, torch.float32, (B, Hkv, weights.shape[-1]))
-    if weights_out is not None:
-        _want("weights_out", weights_out, torch.float32, weights.shape)
-    if dst_block_table is not None:
-        _want("dst_block_table", dst_block_table, torch.int32, block_table.shape)
-    ref = _cache_call(*fields, 0, weights.shape[-1])[1]
-    if kept is None:
-        kept = kv_lens.new_empty((B, Hkv, max(budget, 0)))
-    else:
-        _want("kept", kept, torch.int32, (B, Hkv, budget))
-    if new_kv_lens is None:
-        new_kv_lens = torch.empty_like(kv_lens)
-    else:
-        _want("new_kv_lens", new_kv_lens, torch.int32, (B,))
-    s = lib().tv_evict_cache(ref, budget, int(sink), int(recent), k_cache.data_ptr(),
-                             v_cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), weights.data_ptr(),
-                             _addr(dst_block_table), _addr(weights_out), kept.data_ptr(), new_kv_lens.data_ptr(),
-                             _addr(dev_status), raw)
-    if s != TV_OK:
-        raise TreeVerifyError(s, "tv_evict_cache")
-    return new_kv_lens, kept
-
-
-def _node_stride(name, t, B, N, H, D):
-    """Elements between consecutive nodes of [B][N][H][D]: heads contiguous, sequences N nodes apart."""
-    if t.is_contiguous():
-        return 0
-    sb, st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
-        raise ValueError(f"{name}: the heads of a node must be contiguous")
-    if N == 1:
-        return sb if B > 1 else 0
-    if B > 1 and sb != N * st:
-        raise ValueError(f"{name}: sequences must lie num_nodes nodes apart")
-    return st
+    return _native().evict_cache(k_cache, v_cache, block_table, kv_lens, weights, budget, sink, recent,
+                                 dst_block_table, weights_out, kept, new_kv_lens, max_kv_len, dev_status, stream)
 
 
 def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=None, q_out=None, parent_idx=None,
@@ -759,68 +623,8 @@ def rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q=N
     the caches at prefix_lens[b] + j; returns q_out (None without q).  inv_freq
     [rotary_dim / 2] float32; positions [axes][B][N] int32, or None: the base
     (position_base, else prefix_lens) plus the node's depth under parent_idx (None: chains);
-    axis_of_pair: the axis of each frequency (a sequence of rotary_dim / 2 integers; None:
-    axis 0)."""
-    raw, ctx = _on_gpu(stream, k, (v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx,
-                                   positions, position_base, node_counts, dev_status))
-    if ctx is not None:
-        with ctx:
-            return _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx,
-                           positions, position_base, axis_of_pair, interleaved, node_counts, dev_status)
-    return _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
-                   position_base, axis_of_pair, interleaved, node_counts, dev_status)
-
-
-def _rotary(raw, k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions,
-            position_base, axis_of_pair, interleaved, node_counts, dev_status):
-    import torch
-    if k.dim() != 4 or v.shape != k.shape or k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
-        raise TypeError("k and v must be [batch][nodes][num_kv_heads][head_dim] of the caches' type")
-    B, N, Hkv, D = k.shape
-    Hq, q_stride = Hkv, 0
-    if q is not None:
-        Hq = q.shape[2] if q.dim() == 4 else 0
-        if q.dtype != k.dtype or q.shape != (B, N, Hq, D):
-            raise TypeError("q must be [batch][nodes][num_q_heads][head_dim] of k's type")
-        q_stride = _node_stride("q", q, B, N, Hq, D)
-    fields = _cache_fields(k_cache, v_cache, block_table, Hq, 0.0, 0)
-    if fields[0] != B or fields[2] != Hkv or fields[3] != D:
-        raise ValueError("k, block_table and the caches disagree on batch, heads or head_dim")
-    pairs, axes, num_axes, counts = inv_freq.numel(), b"", 1, None
-    if pairs > 128:
-        raise ValueError("inv_freq must have at most 128 entries")
-    _want("inv_freq", inv_freq, torch.float32, (pairs,))
-    _want("prefix_lens", prefix_lens, torch.int32, (B,))
-    if position_base is not None:
-        _want("position_base", position_base, torch.int32, (B,))
-    if parent_idx is not None:
-        _want("parent_idx", parent_idx, torch.int32, (B, N))
-    if node_counts is not None:
-        _want("node_counts", node_counts, torch.int32, (B,))
-        counts = node_counts.data_ptr()
-    if axis_of_pair is not None:
-        axes = bytes(axis_of_pair)
-        if len(axes) != pairs:
-            raise ValueError("axis_of_pair must have an entry for each of inv_freq")
-        num_axes = max(axes, default=0) + 1
-    if positions is not None:
-        if positions.shape[0] < num_axes:
-            raise ValueError("axis_of_pair names an axis that positions lacks")
-        num_axes = positions.shape[0]
-        _want("positions", positions, torch.int32, (num_axes, B, N))
-    rot = (N, 2 * pairs, 1 if interleaved else 0, num_axes, q_stride, _node_stride("k", k, B, N, Hkv, D),
-           _node_stride("v", v, B, N, Hkv, D), counts)
-    # with counts, their address is in the descriptor: it is this call's own
-    rot, rot_ref = (_rotary_call if counts is None else _rotary_call.__wrapped__)(*rot, axes=axes)
-    ref = _cache_call(*fields, 0, 0)[1]
-    if q_out is not None:
-        _want("q_out", q_out, k.dtype, (B, N, Hq, D))
-    elif q is not None:
-        q_out = q.new_empty((B, N, Hq, D))
-    s = lib().tv_rotary_write(ref, rot_ref, _addr(q), k.data_ptr(), v.data_ptr(), inv_freq.data_ptr(),
-                              _addr(parent_idx), _addr(positions), _addr(position_base), prefix_lens.data_ptr(),
-                              block_table.data_ptr(), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-                              _addr(dev_status), raw)
-    if s != TV_OK:
-        raise TreeVerifyError(s, "tv_rotary_write")
-    return q_out
+    axis_of_pair: the axis of each frequency (bytes or a sequence of rotary_dim / 2 integers;
+    None: axis 0)."""
+    return _native().rotary_write(k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx,
+                                  positions, position_base, None if axis_of_pair is None else bytes(axis_of_pair),
+                                  interleaved, node_counts, dev_status, stream)

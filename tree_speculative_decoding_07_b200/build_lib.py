@@ -1,10 +1,13 @@
-"""Build libtreeverify.so in-tree with nvcc for sm_100a."""
+"""Build libtreeverify.so in-tree with nvcc for sm_100a, and the Python binding's marshalling
+module (_marshal.so) with the host compiler against torch's headers."""
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,10 @@ NVCC_FLAGS = [
     # host arithmetic rounds each operation (the tree-shape DP compares sums exactly)
     "-Xcompiler", "-ffp-contract=off",
 ]
+
+
+MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 
 def sources():
@@ -45,5 +52,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Needs libtreeverify.so (it is linked to it) and torch's headers and libraries."""
+    deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "treeverify.h")]
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    import torch
+    base = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-o", MARSHAL, MARSHAL_SRC, "-L", PKG, "-l:libtreeverify.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    return MARSHAL
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True)
+    build_marshal(force="--force" in sys.argv, verbose=True)

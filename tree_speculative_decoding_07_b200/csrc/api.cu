@@ -206,9 +206,9 @@ tv_status decode_layout(const tv_cache_desc* d, bool weights, DecodeLayout* y) {
     tv::decode_plan(d->dtype, d->batch, d->num_kv_heads, G, d->head_dim, max_len, weights, device_sms(), &p);
     const int64_t tiles = (int64_t)d->batch * d->num_kv_heads * p.NG * ((max_len + 15) / 16);
     if (tiles > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
-    if (p.cluster) {  // the scores alone (and never nothing, so that a caller always has a workspace)
+    if (p.cluster) {  // the scores alone
         y->lse2 = y->ml = y->o = y->scores = 0;
-        y->bytes = weights ? align256(sizeof(float) * (size_t)tiles * 16 * p.GS) : 256;
+        y->bytes = weights ? align256(sizeof(float) * (size_t)tiles * 16 * p.GS) : 0;
         return TV_OK;
     }
     y->lse2 = align256(sizeof(int32_t) * ((size_t)d->batch + 1));
@@ -481,6 +481,7 @@ tv_status tv_decode_attention_plan(const tv_cache_desc* desc, int32_t with_weigh
     if (s != TV_OK) return s;
     if (!plan) return TV_ERR_INVALID_ARG;
     plan->grid_ctas = y.plan.grid;
+    plan->cluster_ctas = y.plan.cluster;
     plan->heads_per_unit = y.plan.HT;
     plan->launches = y.plan.cluster ? 1 : 2;
     plan->smem_bytes = y.plan.smem;
@@ -502,7 +503,7 @@ tv_status tv_decode_attention(const tv_cache_desc* desc, const void* q, const vo
     if (s != TV_OK) return s;
     if (!q || !paged_k || !paged_v || !block_table || !kv_lens || !out || out == q) return TV_ERR_INVALID_ARG;
     if (misaligned(q) || misaligned(paged_k) || misaligned(paged_v) || misaligned(out)) return TV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < y.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    if (y.bytes && (!workspace || workspace_bytes < y.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return TV_ERR_WORKSPACE;
     tv::DecodeArgs a = {};
     a.q = q; a.k = paged_k; a.v = paged_v; a.c = cache_view(desc, block_table); a.lens = kv_lens;
