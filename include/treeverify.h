@@ -608,7 +608,8 @@ TV_API tv_status tv_decode_attention(const tv_cache_desc *desc, const void *q, c
  *                    padded with -1
  *   new_kv_lens      [batch] int32, written: min(kv_lens[b], budget); not kv_lens
  * 0 <= sink, 0 <= recent, sink + recent <= budget, 1 <= budget.  max_kv_len (or the
- * table's capacity) is at most TV_EVICT_MAX_LEN, else TV_ERR_UNSUPPORTED.  A
+ * table's capacity) is at most TV_EVICT_MAX_LEN and budget at most 2^30, else
+ * TV_ERR_UNSUPPORTED.  A
  * length outside [0, max_kv_len] or a block id out of range (in either table)
  * leaves the sequence as it was: kept all -1, new_kv_lens[b] = kv_lens[b], and
  * TV_ERR_INVALID_ARG or TV_ERR_BLOCK_TABLE in *dev_status.  Two launches, no

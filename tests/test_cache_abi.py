@@ -131,6 +131,7 @@ def test_evict_refuses_bad_arguments():
     assert _evict(d, table=A, dst=A) == tv.TV_ERR_INVALID_ARG
     long = _desc(max_blocks_per_seq=tv.TV_EVICT_MAX_LEN // 16 + 1)
     assert _evict(long) == tv.TV_ERR_UNSUPPORTED
+    assert _evict(d, budget=2 ** 30) == tv.TV_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("kw,status", [

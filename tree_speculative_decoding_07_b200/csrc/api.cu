@@ -540,8 +540,9 @@ tv_status tv_evict_cache(const tv_cache_desc* desc, int32_t budget, int32_t sink
     if (misaligned(paged_k) || misaligned(paged_v)) return TV_ERR_INVALID_ARG;
     const int32_t max_len = cache_max_len(desc);
     if (max_len > tv::evict_max_len()) return TV_ERR_UNSUPPORTED;
-    if ((int64_t)desc->batch * desc->num_kv_heads * ((budget + 31LL) / 32) * 2 > INT32_MAX ||
-        (int64_t)desc->batch * desc->num_kv_heads * 16 > INT32_MAX) return TV_ERR_UNSUPPORTED;
+    if (budget > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
+    const int64_t most = budget < max_len ? budget : max_len;  // rows of a head; a CTA moves at least 32
+    if ((int64_t)desc->batch * desc->num_kv_heads * (most / 32 + 16) * 2 > INT32_MAX) return TV_ERR_UNSUPPORTED;
     tv::EvictArgs a = {};
     a.k = paged_k; a.v = paged_v; a.c = cache_view(desc, block_table); a.dst_table = dst_block_table;
     a.lens = kv_lens; a.weights = weights; a.weights_out = weights_out; a.kept = kept; a.new_lens = new_kv_lens;

@@ -36,7 +36,7 @@ constexpr int SE_MAX_CLUSTER = 16;
 constexpr int SE_MAX_SLICE = 49152;  // sums in one CTA's shared memory (192 KB)
 constexpr int BINS = 2048;
 constexpr int SE_UN = 4;             // 16-byte loads of sums that a thread has in flight
-constexpr int SE_STEP = 128;         // sums a warp handles at once, four neighbours per lane
+constexpr int SE_STEP = 128;         // slices are multiples of this many sums
 
 // Order-preserving key of a sum: larger sums, larger keys; NaN 0; -0 as +0.
 __device__ __forceinline__ uint32_t sum_key(float w) {
@@ -47,13 +47,20 @@ __device__ __forceinline__ float key_sum(uint32_t key) {
     return __uint_as_float(key == 0 ? 0x7fc00000u : key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
+// A predicated store (branches would keep the ones after it waiting).
+__device__ __forceinline__ void store_if(bool yes, void* p, int32_t x) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p st.global.s32 [%1], %2;\n}" ::"r"((int)yes), "l"(p),
+                 "r"(x)
+                 : "memory");
+}
+
 struct SelectShared {
     uint32_t own[BINS];         // this CTA's counts of the current digit
     uint32_t total[3][BINS];    // the cluster's; CTA c keeps those of bins c * BINS / C and on
     uint32_t scan[SE_WARPS];
     uint2 warp_cnt[SE_WARPS];   // kept for certain, equal to the threshold
     uint2 cta_cnt;              // the CTA's sums of those, read by its peers
-    uint32_t digit, above;
+    uint32_t digit, above, whole;  // the threshold's digit, the keys above it, whether all keys that have it are kept
     int bad;
 };
 
@@ -87,6 +94,19 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
     const int want = cut ? a.budget - a.sink - a.recent : 0;
     // candidates: lo <= t < lo + span, as one unsigned comparison
     const uint32_t lo = cut ? a.sink : 0, span = cut ? L - a.recent - a.sink : 0;
+    // block ids of the span that is read and of the one that is written
+    {
+        const int32_t* bt = a.c.table + (size_t)b * a.c.max_blocks;
+        const int32_t* dt = a.dst_table ? a.dst_table + (size_t)b * a.c.max_blocks : nullptr;
+        const int nb = (int)(((int64_t)L + a.c.block_size - 1) / a.c.block_size);
+        const int nd = dt ? (int)(((int64_t)n + a.c.block_size - 1) / a.c.block_size) : 0;
+        int bad = 0;
+        for (int i = rank * SE_THREADS + tid; i < nb; i += C * SE_THREADS)
+            bad |= bt[i] < 0 || bt[i] >= a.c.num_blocks;
+        for (int i = rank * SE_THREADS + tid; i < nd; i += C * SE_THREADS)
+            bad |= dt[i] < 0 || dt[i] >= a.c.num_blocks;
+        if (bad) s.bad = 1;
+    }
     // this CTA's slice of the sums
     const int slice = ((L + C - 1) / C + SE_STEP - 1) / SE_STEP * SE_STEP;
     const int t0 = min(L, rank * slice), t1 = min(L, t0 + slice), len = t1 - t0;
@@ -117,19 +137,6 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             for (int e = 0; e < 4; ++e)
                 if (want && (uint32_t)(t0 + y + e) - lo < span && y + e < len) atomicAdd(&s.own[ks[e] >> 21], 1u);
         }
-    }
-    // block ids of the span that is read and of the one that is written
-    {
-        const int32_t* bt = a.c.table + (size_t)b * a.c.max_blocks;
-        const int32_t* dt = a.dst_table ? a.dst_table + (size_t)b * a.c.max_blocks : nullptr;
-        const int nb = (int)(((int64_t)L + a.c.block_size - 1) / a.c.block_size);
-        const int nd = dt ? (int)(((int64_t)n + a.c.block_size - 1) / a.c.block_size) : 0;
-        int bad = 0;
-        for (int i = rank * SE_THREADS + tid; i < nb; i += C * SE_THREADS)
-            bad |= bt[i] < 0 || bt[i] >= a.c.num_blocks;
-        for (int i = rank * SE_THREADS + tid; i < nd; i += C * SE_THREADS)
-            bad |= dt[i] < 0 || dt[i] >= a.c.num_blocks;
-        if (bad) s.bad = 1;
     }
     __syncthreads();
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
                     if (before < left && left <= before + c[e]) {
                         s.digit = bin0 + 3 - e;
                         s.above = before;
+                        s.whole = left == before + c[e];
                     }
                     before += c[e];
                 }
@@ -194,28 +202,24 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
             __syncthreads();
             threshold |= s.digit << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
             left -= s.above;
+            if (s.whole) {  // every key that begins like this is kept, whatever its other digits: the usual end
+                --threshold;  // not 0: there are more candidates than are kept
+                left = 0;
+                break;
+            }
         }
     }
-    // kept for certain: not a candidate, or above the threshold; x in the low half, equals in the high one
-    auto classify = [&](int y, const uint32_t* ks, uint32_t* f) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool sure = (uint32_t)(t0 + y + e) - lo >= span || ks[e] > threshold;
-            f[e] = y + e >= len ? 0u : sure ? 1u : ks[e] == threshold ? 0x10000u : 0u;
-        }
-    };
-    const int per = ((len + SE_WARPS - 1) / SE_WARPS + SE_STEP - 1) / SE_STEP * SE_STEP;
+    // kept for certain: not a candidate, or above the threshold
+    auto sure = [&](int y, uint32_t key) { return (uint32_t)(t0 + y) - lo >= span || key > threshold; };
+    const int per = ((len + SE_WARPS - 1) / SE_WARPS + 31) / 32 * 32;
     const int w0 = min(len, warp * per), w1 = min(len, w0 + per);  // this warp's part of the slice
     uint32_t nk = 0, ne = 0;
-#pragma unroll 1
-    for (int y = w0 + lane * 4; y < w1; y += SE_STEP) {
-        const uint4 k = *reinterpret_cast<const uint4*>(s_key + y);
-        const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
-        uint32_t f[4];
-        classify(y, ks, f);
-        const uint32_t c = f[0] + f[1] + f[2] + f[3];
-        nk += c & 0xffffu;
-        ne += c >> 16;
+#pragma unroll 4
+    for (int y = w0 + lane; y < w1; y += 32) {
+        const uint32_t key = s_key[y];
+        const bool k = sure(y, key);
+        nk += k;
+        ne += !k && key == threshold;
     }
     nk = __reduce_add_sync(0xffffffffu, nk);
     ne = __reduce_add_sync(0xffffffffu, ne);
@@ -252,37 +256,53 @@ __global__ void __launch_bounds__(SE_THREADS) evict_select_kernel(const __grid_c
         for (int r = rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
     } else {
         float* wo = a.weights_out ? a.weights_out + (size_t)bh * a.weight_stride : nullptr;
+        const uint32_t below = (1u << lane) - 1;
+        // Four groups of 32 positions at once, one position per lane: the votes' latencies overlap.
 #pragma unroll 1
-        for (int y0 = w0; y0 < w1; y0 += SE_STEP) {
-            const int y = y0 + lane * 4;
-            const uint4 kv = y < w1 ? *reinterpret_cast<const uint4*>(s_key + y) : make_uint4(0, 0, 0, 0);
-            const uint32_t ks[4] = {kv.x, kv.y, kv.z, kv.w};
-            uint32_t f[4];
-            classify(y, ks, f);
-            const uint32_t c = f[0] + f[1] + f[2] + f[3];
-            uint32_t inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t z = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += z;
-            }
-            uint32_t k = bk + ((inc - c) & 0xffffu), q = be + ((inc - c) >> 16);  // before this lane's four
+        for (int y0 = w0; y0 < w1; y0 += 128) {
+            uint32_t key[4], r[4], equal = 0;
+            bool take[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool take = f[e] == 1u || (f[e] && q < left);
-                const uint32_t r = k + min(q, left);
-                if (take) kept[r] = t0 + y + e;
-                if (take && wo) wo[r] = key_sum(ks[e]);
-                k += f[e] & 1u;
-                q += f[e] >> 16;
+                const int y = y0 + 32 * e + lane;
+                key[e] = y < w1 ? s_key[y] : 0;
+                take[e] = y < w1 && sure(y, key[e]);
+                equal |= (uint32_t)(y < w1 && !take[e] && key[e] == threshold) << e;
             }
-            const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
-            bk += all & 0xffffu;
-            be += all >> 16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t kb = __ballot_sync(0xffffffffu, take[e]);
+                r[e] = bk + __popc(kb & below);
+                bk += __popc(kb);
+            }
+            if (left) {  // equals of the threshold: the first `left` of them
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool eq = equal >> e & 1;
+                    const uint32_t eb = __ballot_sync(0xffffffffu, eq), mine = be + __popc(eb & below);
+                    take[e] |= eq && mine < left;
+                    r[e] += min(mine, left);
+                    be += __popc(eb);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                store_if(take[e], kept + r[e], t0 + y0 + 32 * e + lane);
+                store_if(take[e] && wo, wo + r[e], (int32_t)__float_as_uint(key_sum(key[e])));
+            }
         }
         for (int r = n + rank * SE_THREADS + tid; r < a.budget; r += C * SE_THREADS) kept[r] = -1;
-        if (wo)
-            for (int t = max(t0, n) + tid; t < t1; t += SE_THREADS) wo[t] = 0.f;
+        if (wo) {
+            const int z0 = max(t0, n), zv = vec ? min(t1, (z0 + 3) / 4 * 4) : t1;  // vec: then rows of sums are 16-byte aligned
+            if (!vec)
+                for (int t = z0 + tid; t < t1; t += SE_THREADS) wo[t] = 0.f;
+            else if (tid < 4 && z0 + tid < zv) wo[z0 + tid] = 0.f;
+            for (int t = zv + tid * 4; t < t1; t += 4 * SE_THREADS) {
+                if (t + 4 <= t1) *reinterpret_cast<float4*>(wo + t) = make_float4(0.f, 0.f, 0.f, 0.f);
+                else
+                    for (int e = t; e < t1; ++e) wo[e] = 0.f;
+            }
+        }
         if (lead) a.new_lens[b] = n;
     }
     __syncwarp();
@@ -305,36 +325,34 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_con
     extern __shared__ __align__(16) uint4 mv_ring[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int unit = blockIdx.x / ctas, part = blockIdx.x - unit * ctas, bh = unit / 2, b = bh / a.Hkv, h = bh - b * a.Hkv;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t L = a.lens[b];
-    if (L < 0 || L > a.max_len) return;
-    const int n = L < a.budget ? L : a.budget;
-    if (IN_PLACE && n == L) return;  // nothing moves
+    const int n = L < 0 || L > a.max_len ? 0 : min(L, a.budget);
     const int32_t* kept = a.kept + (size_t)bh * a.budget;
-    if (n == 0 || kept[0] < 0) return;  // flagged by the selection
     const int32_t* bt = a.c.table + (size_t)b * a.c.max_blocks;
     const int32_t* dt = IN_PLACE ? bt : a.dst_table + (size_t)b * a.c.max_blocks;
     const int cpr = a.row_bytes / 16;
     const int rows = min(32, MV_STAGE / a.row_bytes);  // rows of a warp's step, one lane's offsets each
     char* base = static_cast<char*>(unit & 1 ? a.v : a.k) + (int64_t)h * a.c.head_stride;
-    auto row_off = [&](const int32_t* tab, int t) {
-        const int blk = t / a.c.block_size;
-        return (int64_t)tab[blk] * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
-    };
     uint4* ring = mv_ring + warp * (MV_STAGES * MV_STAGE / 16);
     const int chunk = rows * MV_WARPS * ctas, first = (part * MV_WARPS + warp) * rows;
     const int pieces = rows * cpr, drow = 32 / cpr, dpiece = 32 - drow * cpr;
     const int row0 = lane / cpr, piece0 = lane - row0 * cpr;
     const int steps = (n + chunk - 1) / chunk;
-    // lane's row of step s: where it comes from and goes to (-1: nothing to move)
-    auto offsets = [&](int s, int64_t& src, int64_t& dst) {
-        src = dst = -1;
+    // lane's row of step s: where it goes to (-1: there is none), and where it comes from (-1: nothing to move)
+    auto target = [&](int s) -> int64_t {
         const int r = s * chunk + first + lane;
-        if (s >= steps || lane >= rows || r >= n) return;
+        if (lane >= rows || r >= n) return -1;
+        const int blk = r / a.c.block_size, id = dt[blk];
+        if (id < 0 || id >= a.c.num_blocks) return -1;  // the selection reports it
+        return (int64_t)id * a.c.block_stride + (int64_t)(r - blk * a.c.block_size) * a.c.token_stride;
+    };
+    auto source = [&](int s) -> int64_t {
+        const int r = s * chunk + first + lane;
+        if (lane >= rows || r >= n) return -1;
         const int t = kept[r];
-        if (IN_PLACE && t == r) return;
-        src = row_off(bt, t);
-        dst = row_off(dt, r);
+        if (t < 0 || t >= L || (IN_PLACE && t == r)) return -1;  // a flagged sequence, or in place already
+        const int blk = t / a.c.block_size;
+        return (int64_t)bt[blk] * a.c.block_stride + (int64_t)(t - blk * a.c.block_size) * a.c.token_stride;
     };
     auto load = [&](int stage, int64_t src) {
         int row = row0, piece = piece0;
@@ -350,16 +368,20 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_con
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int64_t src, dst, src_next, dst_next, dst_cur;
-    offsets(0, src, dst_cur);
+    // the targets do not depend on the selection
+    int64_t dst = target(0), dst_next = target(1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n == 0 || (IN_PLACE && n == L)) return;  // nothing moves: the same for the whole cluster
+    int64_t src = source(0), src_next = source(1);
     load(0, src);
-    offsets(1, src_next, dst_next);
     for (int s = 0; s < steps; ++s) {
         if (s + 1 < steps) load((s + 1) % MV_STAGES, src_next);
         else asm volatile("cp.async.commit_group;" ::: "memory");
-        dst = dst_cur;
-        dst_cur = dst_next;
-        offsets(s + 2, src_next, dst_next);
+        const int64_t src_now = src, dst_now = dst;
+        src = src_next;
+        dst = dst_next;
+        dst_next = target(s + 2);
+        src_next = source(s + 2);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         if (IN_PLACE) {  // all of this step has been read
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_con
         int row = row0, piece = piece0;
         const uint4* st = ring + (s % MV_STAGES) * (MV_STAGE / 16);
         for (int x = lane; x - lane < pieces; x += 32) {
-            const int64_t o = __shfl_sync(0xffffffffu, dst, row & 31);
+            const int64_t o = __shfl_sync(0xffffffffu, src_now < 0 ? -1 : dst_now, row & 31);
             if (x < pieces && o >= 0) *reinterpret_cast<uint4*>(base + o + piece * 16) = st[x];
             row += drow;
             piece += dpiece;
@@ -410,7 +432,7 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     // four per SM.  At 128K sums and 8 heads clusters of 4, 8 and 16 took (with the move) 63, 50
     // and 49 us; above 8, which not every part of the GPU can place, only for what would not fit.
     int C = 1;
-    while (C < 8 && (int64_t)C * 2048 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
+    while (C < 8 && (int64_t)C * 4096 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
     while ((int64_t)C * SE_MAX_SLICE < a.max_len) C *= 2;
     const size_t smem = sizeof(uint32_t) * ((((size_t)a.max_len + C - 1) / C + SE_STEP - 1) / SE_STEP * SE_STEP);
     static SmemLimit limit;  // the largest slice's, for every call
@@ -418,12 +440,14 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     if (e == cudaSuccess && C > 8)
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    int vec = a.weight_stride % 4 == 0 && !(reinterpret_cast<uintptr_t>(a.weights) & 15);
+    int vec = a.weight_stride % 4 == 0 &&
+              !((reinterpret_cast<uintptr_t>(a.weights) | reinterpret_cast<uintptr_t>(a.weights_out)) & 15);
     void* args[] = {const_cast<EvictArgs*>(&a), &vec};
     e = launch((const void*)evict_select_kernel, (unsigned)(heads * C), C, SE_THREADS, smem, false, st, args);
     if (e != cudaSuccess) return e;
     const int rows = (MV_STAGE / a.row_bytes < 32 ? MV_STAGE / a.row_bytes : 32) * MV_WARPS;  // of a CTA's step
     int ctas = 1;
+    const int most = a.budget < a.max_len ? a.budget : a.max_len;  // rows of a head
     const int ring = MV_WARPS * MV_STAGES * MV_STAGE;
     void* margs[] = {const_cast<EvictArgs*>(&a), &ctas};
     // Steps of 4 KB in 8 warps.  Selection and move together, four cases (4K in place, 8 x 8K
@@ -432,14 +456,14 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     // Copies: two steps per CTA (one 64 us at 8 x 8K, three 60).  In place: a cluster of up to 8,
     // while the GPU has no 8 CTAs per SM (4: 258 us on the mixed case, 16: 254).
     if (a.dst_table) {
-        ctas = (a.budget + 2 * rows - 1) / (2 * rows);
+        ctas = (most + 2 * rows - 1) / (2 * rows);
         static SmemLimit copy_limit;
         e = copy_limit.allow((const void*)evict_move_kernel<false>, ring);
         if (e != cudaSuccess) return e;
         return launch((const void*)evict_move_kernel<false>, (unsigned)(2 * heads * ctas), 1, MV_THREADS, ring, true, st,
                       margs);
     }
-    while (ctas < 8 && ctas * rows < a.budget && (int64_t)2 * heads * ctas < 8LL * sms) ctas *= 2;
+    while (ctas < 8 && ctas * rows < most && (int64_t)2 * heads * ctas < 8LL * sms) ctas *= 2;
     static SmemLimit place_limit;
     e = place_limit.allow((const void*)evict_move_kernel<true>, ring);
     if (e != cudaSuccess) return e;
