@@ -55,8 +55,16 @@ template <typename T, int D> struct Shape {
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// K and V pass through L2 once: first to leave, so that scores and partial results stay.
+__device__ __forceinline__ uint64_t stream_policy() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+                 "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -251,6 +259,7 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
 
     unsigned char* ring = ring_all + warp * S::RING;
     const uint32_t ring_a = smem_u32(ring);
+    const uint64_t policy = stream_policy();
 
     do {
         const int n = min(T_b - t0, end - pos);  // tiles of this piece (none for a CTA that a short sequence leaves over)
@@ -284,8 +293,8 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                 const int64_t o = __shfl_sync(0xffffffffu, off, row);
                 const int bytes = o < 0 ? 0 : 16;  // rows past the sequence are zeros
                 const int64_t at = (o < 0 ? 0 : o) + ch * 16;
-                cp_async16(dst + row * S::ROW + ch * 16, kb + at, bytes);
-                cp_async16(dst + TILE * S::ROW + row * S::ROW + ch * 16, vb + at, bytes);
+                cp_async16(dst + row * S::ROW + ch * 16, kb + at, bytes, policy);
+                cp_async16(dst + TILE * S::ROW + row * S::ROW + ch * 16, vb + at, bytes, policy);
             }
         };
         // block ids of the first tiles and the queries: independent loads, all under way together
