@@ -13,8 +13,8 @@
 // sum and unnormalised output in the workspace, and a second kernel joins
 // them in stretch order (so the result does not depend on timing).
 //
-// Inside a CTA the four warps take tiles in turn.  Each warp keeps its own ring
-// of tiles (cp.async, three deep) and its own running softmax, so there is no
+// Inside a CTA the warps take tiles in turn.  Each warp keeps its own ring
+// of tiles (cp.async, two or three deep) and its own running softmax, so there is no
 // block barrier in the loop.
 //
 // bf16 and fp16 use warp-level matrix instructions (m16n8k16): S^T = K Q^T with
@@ -35,7 +35,6 @@ namespace tv {
 namespace {
 
 constexpr int TILE = 16;              // tokens per step of a warp
-constexpr int STAGES = 3;             // ring depth of a warp, in tiles
 constexpr int MIN_TILES = 8;          // a CTA's shortest stretch
 constexpr float LN2 = 0.6931471805599453f;
 // 16-bit path: the exponentials' reference lies 2^7 below the largest score it was set by, and
@@ -49,9 +48,11 @@ template <typename T, int D> struct Shape {
     static constexpr int ROW = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 32);
     static constexpr int CH = D * (int)sizeof(T) / 16;  // 16-byte pieces of a row
     static constexpr int STAGE = 2 * TILE * ROW;        // a tile of K and of V
+    static constexpr int STAGES = sizeof(T) == 2 ? 3 : 2;  // ring depth of a warp, in tiles
     static constexpr int RING = STAGES * STAGE;         // one warp's ring
-    // Warps per CTA: four rings fit the 227 KB of a CTA, but for fp32 rows of 1 KB.
-    static constexpr int NW = RING * 4 <= 224 * 1024 ? 4 : 2;
+    // Warps per CTA: 16-bit types four, for two CTAs per SM at head_dim 128; fp32 as many as fit.
+    static constexpr int FIT = 210 * 1024 / RING;
+    static constexpr int NW = sizeof(T) == 2 ? 4 : FIT < 8 ? FIT : 8;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -298,9 +299,9 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             }
         };
         // block ids of the first tiles and the queries: independent loads, all under way together
-        int64_t off[STAGES];
+        int64_t off[S::STAGES];
 #pragma unroll
-        for (int e = 0; e < STAGES; ++e) off[e] = offset_of(warp + e * NW);
+        for (int e = 0; e < S::STAGES; ++e) off[e] = offset_of(warp + e * NW);
         // queries
         uint32_t qf[MMA ? NT : 1][MMA ? KS : 1][2];
         if constexpr (MMA) {
@@ -322,12 +323,12 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
 
         int nxt = warp;  // next tile to request
 #pragma unroll
-        for (int e = 0; e < STAGES - 1; ++e) {
+        for (int e = 0; e < S::STAGES - 1; ++e) {
             if (nxt < n) issue(e, off[e]);
             cp_commit();
             nxt += NW;
         }
-        int64_t off_next = off[STAGES - 1];
+        int64_t off_next = off[S::STAGES - 1];
 
         // running softmax: a lane of the matrix path has two heads per 8 (columns
         // 2 (lane % 4) and the next); on the fp32 path every lane has all HT
@@ -346,11 +347,11 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
 
         int slot = 0;
         for (int i = warp; i < n; i += NW) {
-            cp_wait<STAGES - 2>();
+            cp_wait<S::STAGES - 2>();
             __syncwarp();
             {  // the slot that the previous step read is free
-                int free_slot = slot + STAGES - 1;
-                if (free_slot >= STAGES) free_slot -= STAGES;
+                int free_slot = slot + S::STAGES - 1;
+                if (free_slot >= S::STAGES) free_slot -= S::STAGES;
                 if (nxt < n) issue(free_slot, off_next);
                 cp_commit();
                 nxt += NW;
@@ -495,16 +496,19 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     float vv[DV];
 #pragma unroll
                     for (int e = 0; e < DV; ++e) vv[e] = reinterpret_cast<const float*>(vr + t * S::ROW)[lane + 32 * e];
+                    float pp[HT];
+#pragma unroll
+                    for (int g = 0; g < HT; g += 4)
+                        *reinterpret_cast<float4*>(pp + g) = *reinterpret_cast<const float4*>(&s_p[warp][t * HT + g]);
 #pragma unroll
                     for (int g = 0; g < HT; ++g) {
-                        const float p = s_p[warp][t * HT + g];
 #pragma unroll
-                        for (int e = 0; e < DV; ++e) o[g][e] = fmaf(p, vv[e], o[g][e]);
+                        for (int e = 0; e < DV; ++e) o[g][e] = fmaf(pp[g], vv[e], o[g][e]);
                     }
                 }
             }
             __syncwarp();
-            if (++slot == STAGES) slot = 0;
+            if (++slot == S::STAGES) slot = 0;
         }
         cp_wait<0>();
         __syncwarp();
@@ -952,9 +956,11 @@ void decode_plan(int dtype, int B, int Hkv, int G, int D, int max_len, bool weig
     else p->HT = G <= 8 || D > 128 ? 8 : 16;
     p->NG = (G + p->HT - 1) / p->HT;
     p->GS = G < p->HT ? G : p->HT;
-    const int ring = STAGES * 2 * TILE * (D * es + (es == 2 ? 16 : 32));
-    p->smem = ring * (ring * 4 <= 224 * 1024 ? 4 : 2);
-    const int fixed = 4096 + (es == 4 ? p->HT * D * 4 + 4 * TILE * p->HT * 4 : 0);  // static and reserved shared memory
+    // as in Shape
+    const int ring = (es == 2 ? 3 : 2) * 2 * TILE * (D * es + (es == 2 ? 16 : 32));
+    const int fit = 210 * 1024 / ring, warps = es == 2 ? 4 : fit < 8 ? fit : 8;
+    p->smem = ring * warps;
+    const int fixed = 4096 + (es == 4 ? p->HT * D * 4 + warps * TILE * p->HT * 4 : 0);  // static and reserved shared memory
     int per_sm = (228 * 1024) / (p->smem + fixed);
     if (per_sm < 1) per_sm = 1;
     if (per_sm > 4) per_sm = 4;
