@@ -21,9 +21,19 @@
 // the tokens as rows and up to 8 query heads as columns, then O^T += V^T P^T; the
 // transposed 8x8 blocks of P come from movmatrix.  P goes into the product as a
 // high and a low 16-bit part, so no precision is lost to its rounding: the bytes
-// of K and V bound this kernel, not the matrix units.  fp32 runs on the CUDA
-// cores (two lanes per token for the scores, lanes over the head's dimensions
-// for the values).
+// of K and V bound this kernel, not the matrix units.  The exponentials' reference
+// is not the running maximum itself: it lies 2^7 below one and moves only when a
+// score passes it by more than 2^15, so most tiles need no shuffles and no
+// rescaling.  P stays below 2^15 (inside fp16, whose small values keep seven more
+// bits than with a reference at the maximum) and the sums far inside fp32.  fp32
+// runs on the CUDA cores (two lanes per token for the scores, lanes over the
+// head's dimensions for the values).
+//
+// Bound: HBM.  32 sequences of 512 to 32,768 tokens (2.32 GB): 376 us, 94 % of the
+// copy bandwidth; one of 131,072 with weights (545 MB): 112 us, of which the
+// first kernel takes about 94 and the weights' pass the rest; one of 4,096
+// (16.8 MB): 10 us, where launches and dependent loads count.  Batches of fp32
+// heads run at 50 to 60 % (instruction latency).
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -315,10 +325,6 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
                     qf[j][kk][1] = hd < heads ? *reinterpret_cast<const uint32_t*>(row + kk * 16 + 8) : 0u;
                 }
             }
-        } else {
-            __syncthreads();
-            for (int i = tid; i < HT * D; i += DE_THREADS) s_q[i] = i < heads * D ? reinterpret_cast<const float*>(q)[i] : 0.f;
-            __syncthreads();
         }
 
         int nxt = warp;  // next tile to request
@@ -329,6 +335,10 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             nxt += NW;
         }
         int64_t off_next = off[S::STAGES - 1];
+        if constexpr (!MMA) {
+            for (int i = tid; i < HT * D; i += DE_THREADS) s_q[i] = i < heads * D ? reinterpret_cast<const float*>(q)[i] : 0.f;
+            __syncthreads();
+        }
 
         // running softmax: a lane of the matrix path has two heads per 8 (columns
         // 2 (lane % 4) and the next); on the fp32 path every lane has all HT
@@ -593,6 +603,10 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
         }
         if constexpr (CLUSTERS) {
             cg::cluster_group cluster = cg::this_cluster();
+            // the old sum of this thread's first token is on its way during the join
+            float* w = a.weights ? a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride : nullptr;
+            const int first_t = t0 * TILE + tid, end_t = min(L, (t0 + n) * TILE);
+            float old = w && first_t < end_t ? w[first_t] : 0.f;
             cluster.sync();
             const size_t at = (size_t)b * a.Hq + h * a.G + g0;
             // every head's common reference, sum and flag, in rank order
@@ -637,14 +651,12 @@ __global__ void __launch_bounds__(Shape<T, D>::NW * 32) decode_kernel(const __gr
             }
             __syncwarp();
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read its peers' parts
-            if (a.weights && !any_bad) {  // one unit per KV head here; this CTA wrote these scores itself
-                float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
+            if (w && !any_bad) {  // one unit per KV head here; this CTA wrote these scores itself
                 const float* scores = a.scores + (size_t)(pos - t0) * TILE * a.GS;
-                const int end_t = min(L, (t0 + n) * TILE);
-                for (int t = t0 * TILE + tid; t < end_t; t += DE_THREADS) {
+                for (int t = first_t; t < end_t; t += DE_THREADS) {
                     float sum = 0.f;
                     for (int g = 0; g < heads; ++g) sum += ex2(scores[(size_t)t * a.GS + g] - s_lse[g]);
-                    w[t] += sum;
+                    w[t] = (t == first_t ? old : w[t]) + sum;
                 }
             }
             __syncwarp();

@@ -20,6 +20,11 @@
 // read before any of it is written (a cluster barrier between), which with the
 // inequality above is all that is needed.  Copies into other blocks need no
 // order and no barrier.
+//
+// Bound: the selection by its chain of some twenty dependent steps (about 7 us at
+// 4,096 sums, 20 us at 131,072), the move by HBM: 8 x 8,190 tokens to 4,001,
+// copied (267 MB), 58 us together, the move at 5.6 TB/s; 32 sequences of 512 to
+// 32,768 to 4,096 in place (1.05 GB), 238 us.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
