@@ -701,6 +701,8 @@ __device__ __forceinline__ int find_seq(const int32_t* cum, int B, int pos, int 
 }
 
 constexpr int JO_THREADS = 128;
+constexpr int JO_UN = 4;      // rows of a thread that are loaded ahead
+constexpr int CUM_MAX = 512;  // sequences whose tile counts a join CTA adds up itself
 constexpr int WT_UN = 4;  // tokens of a thread whose scores are loaded at once
 
 // Joins the pieces of the heads that several CTAs share, and adds the
@@ -716,8 +718,42 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
     __shared__ float s_red[2][JO_THREADS / 32];
     __shared__ float4 s_o[JO_THREADS];
     __shared__ __align__(16) float s_lse[128];
+    // The tiles before each sequence: of a small batch from the lengths, while the first kernel still runs;
+    // of a large one as that kernel wrote them.
+    __shared__ int32_t s_cum[CUM_MAX + 1];
+    __shared__ int s_scan[JO_THREADS / 32];
+    const int32_t* cum = a.cum;
+    if (a.B <= CUM_MAX) {
+        constexpr int RUN = CUM_MAX / JO_THREADS;
+        int t[RUN], sum = 0;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            t[i] = tid * RUN + i < a.B ? tiles_of(a, tid * RUN + i) : 0;
+            sum += t[i];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int before = inc - sum;
+#pragma unroll
+        for (int w = 0; w < JO_THREADS / 32; ++w)
+            if (w < warp) before += s_scan[w];
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            if (tid * RUN + i <= a.B) s_cum[tid * RUN + i] = before;
+            before += t[i];
+        }
+        if (tid == JO_THREADS - 1 && a.B == CUM_MAX) s_cum[CUM_MAX] = before;
+        __syncthreads();
+        cum = s_cum;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int all = a.cum[a.B], total = all * units;
+    const int all = cum[a.B], total = all * units;
     if (total == 0) return;
     const int per = stretch(total, a.grid);
     if ((int)blockIdx.x >= wblocks) {
@@ -726,15 +762,15 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         if (by_unit) {
             b = y / units;
             u = y - b * units;
-            T_b = a.cum[b + 1] - a.cum[b];
-            first = a.cum[b] * units + u * T_b;
+            T_b = cum[b + 1] - cum[b];
+            first = cum[b] * units + u * T_b;
             if (T_b == 0 || first / per == (first + T_b - 1) / per) return;  // empty, or one stretch had it whole
         } else {
             if (y == 0 || (int64_t)y * per >= total) return;
             const int pos = y * per;
-            b = find_seq(a.cum, a.B, pos, units);
-            const int base = a.cum[b] * units;
-            T_b = a.cum[b + 1] - a.cum[b];
+            b = find_seq(cum, a.B, pos, units);
+            const int base = cum[b] * units;
+            T_b = cum[b + 1] - cum[b];
             u = (pos - base) / T_b;
             first = base + u * T_b;
             if (pos == first || pos - per > first) return;  // the unit's first stretch, or a later one than its second
@@ -742,6 +778,17 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         const int h = u / a.NG, g0 = (u - h * a.NG) * HT;
         if (g0 + hd >= a.G) return;
         const Pieces p = pieces_of(first, T_b, per);
+        constexpr int Q = D / 4, GR = JO_THREADS / Q;  // lanes of a row, rows at once
+        const int gr = tid / Q, d = tid - gr * Q;
+        // the first rows are on their way during the maximum
+        float4 row[JO_UN];
+#pragma unroll
+        for (int k = 0; k < JO_UN; ++k) {
+            const int i = p.c0 + gr + k * GR;
+            row[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (gr < GR && i <= p.c1)
+                row[k] = *reinterpret_cast<const float4*>(a.part_o + ((size_t)p.slot(i) * HT + hd) * D + d * 4);
+        }
         // maximum and sum over the pieces
         float M = -INFINITY, bad = 0.f;
         for (int i = p.c0 + tid; i <= p.c1; i += JO_THREADS) {
@@ -765,22 +812,24 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
             bad = fmaxf(bad, s_red[1][w]);
         }
         const float mu = M == -INFINITY ? 0.f : M;
-        constexpr int Q = D / 4, GR = JO_THREADS / Q;  // lanes of a row, rows at once
-        const int gr = tid / Q, d = tid - gr * Q;
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
-        if (gr < GR)
-            for (int i = p.c0 + gr; i <= p.c1; i += GR) {
-                const size_t at = (size_t)p.slot(i) * HT + hd;
-                const float2 ml = a.part_ml[at];
-                const float4 y = *reinterpret_cast<const float4*>(a.part_o + at * D + d * 4);
-                const float f = ex2(ml.x - mu);
-                sum += ml.y * f;
-                r.x += y.x * f;
-                r.y += y.y * f;
-                r.z += y.z * f;
-                r.w += y.w * f;
-            }
+        auto add = [&](int i, const float4& y) {
+            const float2 ml = a.part_ml[(size_t)p.slot(i) * HT + hd];
+            const float f = ex2(ml.x - mu);
+            sum += ml.y * f;
+            r.x += y.x * f;
+            r.y += y.y * f;
+            r.z += y.z * f;
+            r.w += y.w * f;
+        };
+        if (gr < GR) {
+#pragma unroll
+            for (int k = 0; k < JO_UN; ++k)
+                if (p.c0 + gr + k * GR <= p.c1) add(p.c0 + gr + k * GR, row[k]);
+            for (int i = p.c0 + gr + JO_UN * GR; i <= p.c1; i += GR)
+                add(i, *reinterpret_cast<const float4*>(a.part_o + ((size_t)p.slot(i) * HT + hd) * D + d * 4));
+        }
         __shared__ float s_sum[JO_THREADS];
         s_o[tid] = r;
         s_sum[tid] = sum;
@@ -814,16 +863,16 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
     if ((int64_t)wb * wper >= wtotal) return;
     int pos = wb * wper;
     const int end = min(wtotal, pos + wper);
-    int b = find_seq(a.cum, a.B, pos, a.Hkv);
+    int b = find_seq(cum, a.B, pos, a.Hkv);
     while (pos < end) {
-        const int T_b = a.cum[b + 1] - a.cum[b];
-        const int base = a.cum[b] * a.Hkv, h = (pos - base) / T_b, t0 = pos - base - h * T_b;
+        const int T_b = cum[b + 1] - cum[b];
+        const int base = cum[b] * a.Hkv, h = (pos - base) / T_b, t0 = pos - base - h * T_b;
         const int n = min(T_b - t0, end - pos);
         // log-sum-exp of the KV head's query heads, a warp each
         int bad_any = 0;
         __syncthreads();
         for (int g = warp; g < a.G; g += JO_THREADS / 32) {
-            const int k = g / HT, hd = g - k * HT, first = a.cum[b] * units + (h * a.NG + k) * T_b;
+            const int k = g / HT, hd = g - k * HT, first = cum[b] * units + (h * a.NG + k) * T_b;
             const Pieces p = pieces_of(first, T_b, per);
             float x;
             if (p.c0 == p.c1) {
@@ -856,7 +905,7 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
         const int L = a.lens[b];
         float* w = a.weights + ((size_t)b * a.Hkv + h) * a.weight_stride;
         // scores of a token lie side by side: GS for each of the KV head's NG units
-        const float* scores = a.scores + ((size_t)a.cum[b] * units + (size_t)h * a.NG * T_b) * TILE * a.GS;
+        const float* scores = a.scores + ((size_t)cum[b] * units + (size_t)h * a.NG * T_b) * TILE * a.GS;
         const size_t unit_scores = (size_t)T_b * TILE * a.GS;
         auto weight_of = [&](int t) {
             float sum = 0.f;
@@ -901,7 +950,7 @@ __global__ void __launch_bounds__(JO_THREADS) decode_join_kernel(const __grid_co
             }
         }
         pos += n;
-        while (pos < end && pos >= a.cum[b + 1] * a.Hkv) ++b;
+        while (pos < end && pos >= cum[b + 1] * a.Hkv) ++b;
     }
 }
 
