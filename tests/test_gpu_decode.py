@@ -88,6 +88,46 @@ def test_large_ragged_batch(weights):
     _check(Cache(4, rng.integers(0, 700, 130), 2, 64, "f16"), 6, weights)
 
 
+@pytest.mark.parametrize("B", [511, 512, 513, 6000])
+@pytest.mark.parametrize("weights", [False, True])
+def test_batches_of_many_sequences(B, weights):
+    """Sequences that share a pool of blocks (reading needs no blocks of one's own), most of them short, a few
+    long: the equal stretches cover many sequences each.  The reference runs in float64 on the GPU."""
+    rng = np.random.default_rng(B)
+    hkv, g, d, pool, width = 2, 2, 64, 90, 45
+    lens = rng.integers(0, 40, B)
+    lens[rng.integers(0, B, B // 20)] = rng.integers(500, width * 16 + 1, B // 20)
+    lens = lens.astype(np.int32)
+    k, v = (torch.from_numpy(rng.standard_normal((pool, 16, hkv, d)).astype(np.float32)).cuda().bfloat16() for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((B, hkv * g, d)).astype(np.float32)).cuda().bfloat16()
+    table, dl = to_gpu(rng.integers(0, pool, (B, width)).astype(np.int32)), to_gpu(lens)
+    w = torch.rand(B, hkv, width * 16, device="cuda") if weights else None
+    w0 = w.clone() if weights else None
+    out, lse = tv.decode_attention(q, k, v, table, dl, attn_weights=w)
+    for b0 in range(0, B, 500):
+        sel = slice(b0, min(B, b0 + 500))
+        kk = k[table[sel].long()].flatten(1, 2).permute(0, 2, 3, 1).double()  # [b][hkv][d][t]
+        vv = v[table[sel].long()].flatten(1, 2).permute(0, 2, 1, 3).double()
+        qq = q[sel].double().reshape(-1, hkv, g, d)
+        s = (qq @ kk) / 8
+        size = (qq.abs() @ kk.abs()).amax(-1) / 8
+        seen = torch.arange(width * 16, device="cuda") < dl[sel, None]
+        s = s.masked_fill(~seen[:, None, None], -torch.inf)
+        p = torch.nan_to_num(torch.softmax(s, -1))  # empty rows: zeros
+        ref, ref_lse = (p @ vv).reshape(-1, hkv * g, d), torch.logsumexp(s, -1).reshape(-1, hkv * g)
+        ds = (d + 8) * 2 ** -23 * size
+        rel = (2 * ds + 2 ** -21 + 2 ** -16 + 2 * (width + 64) * 2 ** -23)  # as decode_bounds
+        tol = (rel[..., None] * (p @ vv.abs())).reshape(ref.shape) + 2 ** -8 * ref.abs() * 1.01
+        assert ((out[sel].double() - ref).abs() <= tol).all()
+        fine = dl[sel] > 0
+        assert ((lse[sel] - ref_lse).abs()[fine] <= (ds.reshape(ref_lse.shape) + 2 ** -20 + 2 ** -22 * ref_lse.abs())[fine]).all()
+        assert torch.isneginf(lse[sel][~fine]).all()
+        if weights:
+            add = p.sum(2)
+            want_w = w0[sel].double() + add
+            assert ((w[sel] - want_w).abs() <= (rel[..., None] * p).sum(2) + 2 ** -23 * want_w * (add > 0)).all()
+
+
 def test_every_sequence_empty():
     c = Cache(5, [0, 0, 0], 2, 64, "bf16", width=2)
     out, lse, w = _run(c, _queries(c, 4), np.ones((3, 2, 32), np.float32))

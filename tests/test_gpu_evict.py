@@ -104,6 +104,30 @@ def test_the_longest_caches(n):
     _check(Cache(12, [n], 1, 16, "bf16", spare=0), 3001, 5, 64, kind="few values", out="same")
 
 
+@pytest.mark.parametrize("copy", [False, True])
+def test_batches_of_many_sequences(copy):
+    rng = np.random.default_rng(5)
+    _check(Cache(13, rng.integers(0, 60, 900), 2, 16, "bf16", block=8), 25, 2, 5, copy=copy, out="same")
+
+
+def test_two_calls_at_once():
+    """Two caches on two streams, again and again: nothing is shared between calls."""
+    cs = [Cache(14 + i, [3000, 40, 700], 2, 64, "bf16") for i in range(2)]
+    ws = [_sums(c, "few values") for c in cs]
+    refs = [evict_reference(c, w, 300, 3, 20) for c, w in zip(cs, ws)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    start = [(to_gpu(c.k, "bf16"), to_gpu(c.v, "bf16"), to_gpu(c.table), to_gpu(c.lens), to_gpu(w)) for c, w in zip(cs, ws)]
+    for _ in range(5):
+        work = [(k.clone(), v.clone()) for k, v, *_ in start]
+        torch.cuda.synchronize()
+        res = [tv.evict_cache(*work[i], *start[i][2:], 300, 3, 20, stream=streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            np.testing.assert_array_equal(res[i][1].cpu().numpy(), refs[i][3])
+            np.testing.assert_array_equal(_host(work[i][0]), refs[i][0])
+            np.testing.assert_array_equal(_host(work[i][1]), refs[i][1])
+
+
 @pytest.mark.parametrize("kind", ["equal", "few values", "mixed"])
 def test_ties_across_the_slices_of_a_cluster(kind):
     _check(Cache(4, [17000], 1, 16, "bf16"), 8500, 3, 100, kind=kind, out="same")

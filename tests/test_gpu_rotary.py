@@ -147,6 +147,17 @@ def test_one_token_and_a_long_prompt():
     Step(10, 1, 3001, 2, 1, 64, "f16", prefix=[77]).check()
 
 
+def test_batches_of_many_sequences():
+    rng = np.random.default_rng(18)
+    Step(18, 700, 3, 2, 1, 16, "bf16", tree=True, counts=rng.integers(0, 4, 700)).check()
+
+
+def test_a_tree_of_1024_nodes():
+    s = Step(19, 1, 1024, 1, 1, 16, "f32", tree=True)
+    s.parent[0, 700:] = np.arange(699, 1023)  # its tail a chain
+    s.check()
+
+
 def test_in_place_queries_and_no_queries():
     Step(11, 2, 6, 8, 2, 128, "bf16", counts=[6, 3]).check(q_out="same")
     s = Step(12, 2, 6, 8, 2, 128, "bf16")
