@@ -16,7 +16,8 @@
 // heads (403 MB) takes 68 us, 90 % of the copy bandwidth.  That needed few
 // instructions: with a division per 16-byte piece and the cosines read from
 // shared memory for each, it took 107 to 123 us.  A small call is launch and
-// three dependent loads (5 us for one 64-node tree).
+// three dependent loads (4 us for one 64-node tree; 5 with its parents read from
+// global memory, one after the other).
 #include "kernels.h"
 #include "tv_common.cuh"
 
