@@ -18,7 +18,9 @@
 // with r, so for r < r' the destination r <= r' - 1 < src(r').  One cluster per
 // (sequence, KV head) takes the rows in ascending chunks; all of a chunk is
 // read before any of it is written (a cluster barrier between), which with the
-// inequality above is all that is needed.  Copies into other blocks need no
+// inequality above is all that is needed.  From the chunk on whose first source
+// lies past the last destination, nothing that is still to be read can be
+// written any more, and the barriers end.  Copies into other blocks need no
 // order and no barrier.
 //
 // Bound: the selection by its chain of some twenty dependent steps (about 7 us at
@@ -378,6 +380,9 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0 || (IN_PLACE && n == L)) return;  // nothing moves: the same for the whole cluster
     int64_t src = source(0), src_next = source(1);
+    // where the first row of a step (of all CTAs) comes from: the others come from behind it
+    auto head_of = [&](int s) { return (int64_t)s * chunk < n ? kept[s * chunk] : n; };
+    int head = IN_PLACE ? kept[0] : n, head_next = IN_PLACE ? head_of(1) : n;
     load(0, src);
     for (int s = 0; s < steps; ++s) {
         if (s + 1 < steps) load((s + 1) % MV_STAGES, src_next);
@@ -389,9 +394,11 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const __grid_con
         src_next = source(s + 2);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        if (IN_PLACE) {  // all of this step has been read
+        if (IN_PLACE && head < n) {  // all of this step has been read; no barrier once the sources lie past every target
             if (ctas > 1) cg::this_cluster().sync();
             else __syncthreads();
+            head = head_next;
+            head_next = head_of(s + 2);
         }
         int row = row0, piece = piece0;
         const uint4* st = ring + (s % MV_STAGES) * (MV_STAGE / 16);
