@@ -555,7 +555,8 @@ typedef struct {
  * fp32; for bf16 and fp16 the softmax weights enter the product with the
  * values as two 16-bit parts, so only `out` itself is rounded.
  * A sequence with kv_lens[b] = 0 (padding of a batch) gets zeros and an lse
- * of -inf, as does a row whose scores are all -inf.  A length outside
+ * of -inf, as does a row whose scores are all -inf; a NaN score makes its row NaN
+ * (out, lse, and the weights of its KV head).  A length outside
  * [0, max_kv_len] or a block id out of range gives the sequence NaN rows, leaves
  * its attn_weights as they were and writes TV_ERR_INVALID_ARG or
  * TV_ERR_BLOCK_TABLE to *dev_status.  Cache slots past kv_lens[b] are not read.

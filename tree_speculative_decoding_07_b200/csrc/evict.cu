@@ -26,7 +26,7 @@
 // Bound: the selection by its chain of some twenty dependent steps (about 7 us at
 // 4,096 sums, 20 us at 131,072), the move by HBM: 8 x 8,190 tokens to 4,001,
 // copied (267 MB), 58 us together, the move at 5.6 TB/s; 32 sequences of 512 to
-// 32,768 to 4,096 in place (1.05 GB), 238 us.
+// 32,768 to 4,096 in place (1.05 GB), 214 us.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -463,10 +463,10 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     const int ring = MV_WARPS * MV_STAGES * MV_STAGE;
     void* margs[] = {const_cast<EvictArgs*>(&a), &ctas};
     // Steps of 4 KB in 8 warps.  Selection and move together, four cases (4K in place, 8 x 8K
-    // copied, 128K copied, 32 mixed in place): 16.9, 59, 48 and 240 us; 8 KB in 4 warps 16.9, 62,
-    // 50 and 257; 4 KB in 4 warps 19.2, 59, 48 and 256; 8 KB in 8 warps 18.1, 71, 54 and 318.
+    // copied, 128K copied, 32 mixed in place): 13.0, 57.7, 46.6 and 214 us; 4 KB in 4 warps 15.5,
+    // 57.1, 46.4 and 225; 2 KB in 8 warps 14.9, 61, 46.5 and 229; 8 KB in 4 warps 13.5, 60, 48.3 and 225.
     // Copies: two steps per CTA (one 64 us at 8 x 8K, three 60).  In place: a cluster of up to 8,
-    // while the GPU has no 8 CTAs per SM (4: 258 us on the mixed case, 16: 254).
+    // while the GPU has no 8 CTAs per SM (4: 227 us on the mixed case, 16: 232).
     if (a.dst_table) {
         ctas = (most + 2 * rows - 1) / (2 * rows);
         static SmemLimit copy_limit;
