@@ -13,7 +13,7 @@
 // looks up where the rows go and the first R/2 threads form the angles.
 //
 // Bound: HBM (each row is read once and written once): a 16,384-token prompt of 32 + 8 + 8
-// heads (403 MB) takes 68 us, 90 % of the copy bandwidth.  That needed few
+// heads (403 MB) takes 67 us, 92 % of the copy bandwidth.  That needed few
 // instructions: with a division per 16-byte piece and the cosines read from
 // shared memory for each, it took 107 to 123 us.  A small call is launch and
 // three dependent loads (4 us for one 64-node tree; 5 with its parents read from
@@ -25,7 +25,6 @@ namespace tv {
 namespace {
 
 constexpr int RO_THREADS = 128;
-constexpr int MAX_TREE = 1024;  // nodes per sequence with a parent array (checked by the caller)
 constexpr int RO_UN = 3;  // heads of a thread whose loads are under way before the angles are known
 
 // 16 bytes as fp32 values, and back
@@ -94,20 +93,22 @@ __device__ __forceinline__ int node_depth(const int32_t* parent, int j) {
     return parent[0] == -1 ? depth : -1;
 }
 
-template <typename T, bool INTER>
+// TREE: depths from a parent array.  A kernel of its own: with a branch for it, the first loads of
+// a prompt's rows came later (79 us against 68 for 16,384 tokens).
+template <typename T, bool INTER, bool TREE>
 __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int PN = Pack<T>::N;
     constexpr int NF = INTER ? PN / 2 : PN;  // frequencies of a thread's pieces
     __shared__ __align__(16) float s_cos[128], s_sin[128];
     __shared__ long long s_off;
     __shared__ int s_bad;
-    __shared__ int32_t s_parent[MAX_TREE];
+    extern __shared__ int32_t s_parent[];  // with a parent array: N of them
     const int tid = threadIdx.x, b = blockIdx.x / a.N, j = blockIdx.x - b * a.N;
     bool bad_count;
     const int n = seq_nodes(a.counts, b, a.N, bad_count);
     if (j >= n) return;
     const int L = a.prefix_lens[b];
-    if (a.parent)  // the parents that a path from node j can meet
+    if constexpr (TREE)  // the parents that a path from node j can meet
         for (int i = tid; i <= j; i += RO_THREADS) s_parent[i] = a.parent[(size_t)b * a.N + i];
     const size_t node = (size_t)b * a.N + j;
     // A thread keeps to one place of the rows: piece i (and i + Rp / 2), of the heads
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constan
         s_bad = bad;
     }
     int depth = j;
-    if (a.parent) {
+    if constexpr (TREE) {
         __syncthreads();
         depth = node_depth(s_parent, j);
     }
@@ -226,8 +227,14 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_kernel(const __grid_constan
 }
 
 template <typename T> void launch(const RotaryArgs& a, unsigned grid, cudaStream_t st) {
-    if (a.interleaved) rotary_kernel<T, true><<<grid, RO_THREADS, 0, st>>>(a);
-    else rotary_kernel<T, false><<<grid, RO_THREADS, 0, st>>>(a);
+    const size_t parents = sizeof(int32_t) * (size_t)a.N;  // N <= 1024 with parents: checked by the caller
+    if (a.interleaved) {
+        if (a.parent) rotary_kernel<T, true, true><<<grid, RO_THREADS, parents, st>>>(a);
+        else rotary_kernel<T, true, false><<<grid, RO_THREADS, 0, st>>>(a);
+    } else {
+        if (a.parent) rotary_kernel<T, false, true><<<grid, RO_THREADS, parents, st>>>(a);
+        else rotary_kernel<T, false, false><<<grid, RO_THREADS, 0, st>>>(a);
+    }
 }
 
 }  // namespace
