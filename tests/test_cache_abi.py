@@ -214,6 +214,41 @@ def test_wrappers_refuse_host_tensors_and_bad_shapes():
     assert tv.cache_desc(c, c, table).block_stride == 0
 
 
+def test_wrappers_refuse_expanded_rows():
+    """A stride of 0 between sequences or nodes is an expanded tensor's; in the descriptors 0 means contiguous,
+    so passing it on would read past the one row that there is."""
+    c = torch.zeros(4, 16, 2, 64)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    one_q = torch.zeros(1, 4, 64)
+    for q in (one_q.expand(2, 4, 64), torch.zeros(320).as_strided((2, 4, 64), (64, 64, 1))):
+        with pytest.raises(ValueError, match="q: .*overlap"):
+            tv.decode_attention(q, c, c, table, lens)
+    with pytest.raises(ValueError, match="heads"):
+        tv.decode_attention(torch.zeros(2, 1, 64).expand(2, 4, 64), c, c, table, lens)
+    freq = torch.ones(32)
+
+    def rows(b, n, h=2):
+        return torch.zeros(b, n, h, 64)
+
+    for b, n in ((2, 1), (1, 3), (2, 3)):
+        tab, pre = torch.zeros(b, 2, dtype=torch.int32), torch.zeros(b, dtype=torch.int32)
+        whole, q = rows(b, n), rows(b, n, 4)
+        expanded = [rows(1, 1).expand(b, n, 2, 64)]
+        if b > 1 and n > 1:
+            expanded += [rows(1, n).expand(b, n, 2, 64), rows(b, 1).expand(b, n, 2, 64)]
+        for x in expanded:
+            for k, v, name in ((x, whole, "k"), (whole, x, "v")):
+                with pytest.raises(ValueError, match=name + ": .*(overlap|apart)"):
+                    tv.rotary_write(k, v, freq, c, c, tab, pre, q=q)
+        with pytest.raises(ValueError, match="q: .*(overlap|apart)"):
+            tv.rotary_write(whole, whole, freq, c, c, tab, pre, q=rows(1, 1, 4).expand(b, n, 4, 64))
+        with pytest.raises(ValueError, match="CUDA"):  # the same call on rows of their own gets past these checks
+            tv.rotary_write(whole, whole, freq, c, c, tab, pre, q=q)
+    # a single sequence's stride says nothing
+    with pytest.raises(ValueError, match="CUDA"):
+        tv.decode_attention(torch.zeros(1, 4, 64).expand(1, 4, 64), c, c, table[:1], lens[:1])
+
+
 def test_references_against_closed_forms():
     c = Cache(0, [1, 40], 2, 64, "f32")
     q = as_type(c.rng.standard_normal((2, 4, 64)), "f32")

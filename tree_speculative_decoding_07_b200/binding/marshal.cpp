@@ -51,10 +51,12 @@ std::string shape_of(c10::IntArrayRef s) {
     return r + (s.size() == 1 ? ",)" : ")");
 }
 
-// A tensor argument, or nullptr for None.  All of a call's have to lie on one GPU.
+// A tensor argument, or nullptr for None.  All of a call's have to lie on one GPU: Launch refuses
+// host tensors, after the checks of types, shapes and strides, which therefore need no GPU.
 struct Args {
     PyObject* const* v;
     int device = -1;
+    bool on_host = false;
 
     const at::Tensor* tensor(int i, const char* name, bool optional = false) {
         if (v[i] == Py_None) {
@@ -63,8 +65,8 @@ struct Args {
         }
         if (!THPVariable_Check(v[i])) type_error(std::string(name) + " must be a tensor");
         const at::Tensor& t = THPVariable_Unpack(v[i]);
-        if (!t.is_cuda()) value_error("all tensors must be CUDA tensors");
-        if (device < 0) device = t.get_device();
+        if (!t.is_cuda()) on_host = true;
+        else if (device < 0) device = t.get_device();
         else if (t.get_device() != device)
             value_error("all tensors must be on one GPU: cuda:" + std::to_string(device) + " and cuda:" +
                         std::to_string(t.get_device()));
@@ -93,7 +95,9 @@ struct Launch {
     std::optional<c10::cuda::CUDAGuard> device_guard;
     void* stream = nullptr;
 
-    Launch(PyObject* s, int device) {
+    Launch(PyObject* s, const Args& args) {
+        if (args.on_host || args.device < 0) value_error("all tensors must be CUDA tensors");
+        const int device = args.device;
         if (s == Py_None) {
             if (c10::cuda::current_device() != device) device_guard.emplace((c10::DeviceIndex)device);
             stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
@@ -197,6 +201,15 @@ tv_cache_desc cache_desc(const at::Tensor& k, const at::Tensor& v, const at::Ten
     return d;
 }
 
+// A stride between rows, for a descriptor in which 0 means contiguous: an expanded tensor's 0 would be
+// read as that, far past the one row that it has.
+int64_t row_apart(const char* name, const char* of, int64_t stride, int64_t row) {
+    if (stride < row)
+        value_error(std::string(name) + ": the rows of one " + of + " must not overlap the next one's (stride " +
+                    std::to_string(stride) + ", row " + std::to_string(row) + "; call contiguous() on an expanded tensor)");
+    return stride;
+}
+
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
     PyObject* x = THPVariable_Wrap(a);
     PyObject* y = x ? THPVariable_Wrap(b) : nullptr;
@@ -222,7 +235,7 @@ PyObject* decode_attention(Args a) {
     if (!q.is_contiguous()) {
         if ((D > 1 && q.stride(2) != 1) || (Hq > 1 && q.stride(1) != D))
             value_error("q: the heads of a sequence must be contiguous");
-        d.q_stride = B > 1 ? q.stride(0) : 0;
+        if (B > 1) d.q_stride = row_apart("q", "sequence", q.stride(0), Hq * D);
     }
     want("kv_lens", lens, at::kInt, {B});
     if (w) {
@@ -233,7 +246,7 @@ PyObject* decode_attention(Args a) {
     if (status) want("dev_status", *status, at::kInt, status->sizes());
     if (out_p) want("out", *out_p, q.scalar_type(), {B, Hq, D});
     if (lse_p) want("lse", *lse_p, at::kFloat, {B, Hq});
-    Launch launch(a.v[12], a.device);
+    Launch launch(a.v[12], a);
     tv_decode_plan plan;
     check(tv_decode_attention_plan(&d, w != nullptr, &plan), "tv_decode_attention_plan");
     at::Tensor out = out_p ? *out_p : make({B, Hq, D}, q.scalar_type(), a.device);
@@ -274,7 +287,7 @@ PyObject* evict_cache(Args a) {
     if (kept_p) want("kept", *kept_p, at::kInt, {B, H, budget});
     if (new_p) want("new_kv_lens", *new_p, at::kInt, {B});
     if (status) want("dev_status", *status, at::kInt, status->sizes());
-    Launch launch(a.v[14], a.device);
+    Launch launch(a.v[14], a);
     at::Tensor kept = kept_p ? *kept_p : make({B, H, budget > 0 ? budget : 0}, at::kInt, a.device);
     at::Tensor lens_out = new_p ? *new_p : make({B}, at::kInt, a.device);
     check(tv_evict_cache(&d, (int32_t)budget, (int32_t)sink, (int32_t)recent, ptr(k), ptr(v), ptr<int32_t>(table),
@@ -290,10 +303,10 @@ int64_t node_stride(const char* name, const at::Tensor& t) {
     const int64_t B = t.size(0), N = t.size(1), H = t.size(2), D = t.size(3);
     if ((D > 1 && t.stride(3) != 1) || (H > 1 && t.stride(2) != D))
         value_error(std::string(name) + ": the heads of a node must be contiguous");
-    if (N == 1) return B > 1 ? t.stride(0) : 0;
+    if (N == 1) return B > 1 ? row_apart(name, "sequence", t.stride(0), H * D) : 0;
     if (B > 1 && t.stride(0) != N * t.stride(1))
         value_error(std::string(name) + ": sequences must lie num_nodes nodes apart");
-    return t.stride(1);
+    return row_apart(name, "node", t.stride(1), H * D);
 }
 
 // (k, v, inv_freq, k_cache, v_cache, block_table, prefix_lens, q, q_out, parent_idx, positions, position_base,
@@ -353,7 +366,7 @@ PyObject* rotary_write(Args a) {
         r.num_axes = narrow(n, "num_axes");
     }
     if (out_p) want("q_out", *out_p, type, {B, N, Hq, D});
-    Launch launch(a.v[16], a.device);
+    Launch launch(a.v[16], a);
     at::Tensor out;
     if (out_p) out = *out_p;
     else if (q) out = make({B, N, Hq, D}, type, a.device);
