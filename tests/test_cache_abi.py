@@ -249,6 +249,24 @@ def test_wrappers_refuse_expanded_rows():
         tv.decode_attention(torch.zeros(1, 4, 64).expand(1, 4, 64), c, c, table[:1], lens[:1])
 
 
+def test_wrappers_refuse_empty_tensors():
+    """An empty tensor has no address, which the C calls take for an argument that was not given."""
+    c = torch.zeros(4, 16, 2, 64)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q, k = torch.zeros(1, 4, 64), torch.zeros(1, 1, 2, 64)
+    none, empty = torch.zeros(1, 2, 0), torch.zeros(0, dtype=torch.int32)
+    with pytest.raises(ValueError, match="attn_weights"):
+        tv.decode_attention(q, c, c, table, lens, attn_weights=none)
+    with pytest.raises(ValueError, match="weights"):
+        tv.evict_cache(c, c, table, lens, none, 8)
+    with pytest.raises(ValueError, match="dev_status"):
+        tv.decode_attention(q, c, c, table, lens, dev_status=empty)
+    with pytest.raises(ValueError, match="dev_status"):
+        tv.evict_cache(c, c, table, lens, torch.zeros(1, 2, 32), 8, dev_status=empty)
+    with pytest.raises(ValueError, match="dev_status"):
+        tv.rotary_write(k, k, torch.ones(32), c, c, table, lens, dev_status=empty)
+
+
 def test_references_against_closed_forms():
     c = Cache(0, [1, 40], 2, 64, "f32")
     q = as_type(c.rng.standard_normal((2, 4, 64)), "f32")

@@ -136,6 +136,20 @@ void want(const char* name, const at::Tensor& t, at::ScalarType type, c10::IntAr
     if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
 }
 
+// An empty tensor has no address, which the C calls would take for "not given".
+void want_status(const at::Tensor& t) {
+    want("dev_status", t, at::kInt, t.sizes());
+    if (t.numel() == 0) value_error("dev_status must have an element");
+}
+
+// Sums per cached token: [batch][heads][width]; the width.
+int64_t want_sums(const char* name, const at::Tensor& t, int64_t batch, int64_t heads) {
+    const int64_t width = t.dim() ? t.size(-1) : 0;
+    want(name, t, at::kFloat, {batch, heads, width});
+    if (width == 0) value_error(std::string(name) + " must have an entry for every cached token");
+    return width;
+}
+
 at::Tensor make(c10::IntArrayRef shape, at::ScalarType type, int device) {
     return at::empty(shape, at::TensorOptions().dtype(type).device(c10::DeviceType::CUDA, (c10::DeviceIndex)device));
 }
@@ -238,12 +252,8 @@ PyObject* decode_attention(Args a) {
         if (B > 1) d.q_stride = row_apart("q", "sequence", q.stride(0), Hq * D);
     }
     want("kv_lens", lens, at::kInt, {B});
-    if (w) {
-        const int64_t width = w->dim() ? w->size(-1) : 0;
-        want("attn_weights", *w, at::kFloat, {B, d.num_kv_heads, width});
-        d.weight_stride = width;
-    }
-    if (status) want("dev_status", *status, at::kInt, status->sizes());
+    if (w) d.weight_stride = want_sums("attn_weights", *w, B, d.num_kv_heads);
+    if (status) want_status(*status);
     if (out_p) want("out", *out_p, q.scalar_type(), {B, Hq, D});
     if (lse_p) want("lse", *lse_p, at::kFloat, {B, Hq});
     Launch launch(a.v[12], a);
@@ -279,14 +289,13 @@ PyObject* evict_cache(Args a) {
     const int64_t B = d.batch, H = d.num_kv_heads, budget = a.integer(5, "budget");
     const int64_t sink = a.integer(6, "sink"), recent = a.integer(7, "recent");
     want("kv_lens", lens, at::kInt, {B});
-    const int64_t width = w.dim() ? w.size(-1) : 0;
-    want("weights", w, at::kFloat, {B, H, width});
+    const int64_t width = want_sums("weights", w, B, H);
     d.weight_stride = width;
     if (wo) want("weights_out", *wo, at::kFloat, {B, H, width});
     if (dst) want("dst_block_table", *dst, at::kInt, table.sizes());
     if (kept_p) want("kept", *kept_p, at::kInt, {B, H, budget});
     if (new_p) want("new_kv_lens", *new_p, at::kInt, {B});
-    if (status) want("dev_status", *status, at::kInt, status->sizes());
+    if (status) want_status(*status);
     Launch launch(a.v[14], a);
     at::Tensor kept = kept_p ? *kept_p : make({B, H, budget > 0 ? budget : 0}, at::kInt, a.device);
     at::Tensor lens_out = new_p ? *new_p : make({B}, at::kInt, a.device);
@@ -340,7 +349,7 @@ PyObject* rotary_write(Args a) {
     if (base) want("position_base", *base, at::kInt, {B});
     if (parent) want("parent_idx", *parent, at::kInt, {B, N});
     if (counts) want("node_counts", *counts, at::kInt, {B});
-    if (status) want("dev_status", *status, at::kInt, status->sizes());
+    if (status) want_status(*status);
     r.num_nodes = narrow(N, "num_nodes");
     r.rotary_dim = (int32_t)(2 * pairs);
     r.interleaved = PyObject_IsTrue(a.v[13]);
