@@ -519,7 +519,9 @@ TV_API tv_status tv_tree_select_device(int32_t batch, int32_t max_candidates, co
  * slot * token_stride + head * head_stride + dim.  All three 0: the layout
  * [num_blocks][block_size][num_kv_heads][head_dim] of the other calls.
  * Strides times the element size, and the caches' addresses, are multiples of
- * 16 bytes.  Elements of different (block, slot, head) must not overlap.
+ * 16 bytes.  Elements of different (block, slot, head) must not overlap, nor the K
+ * cache and the V cache where rows are written (tv_rotary_write, tv_evict_cache in
+ * place: TV_ERR_INVALID_ARG when both are one address).
  */
 typedef struct {
     int32_t batch;

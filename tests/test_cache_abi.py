@@ -267,6 +267,35 @@ def test_wrappers_refuse_empty_tensors():
         tv.rotary_write(k, k, torch.ones(32), c, c, table, lens, dev_status=empty)
 
 
+def test_writers_refuse_one_cache_for_keys_and_values():
+    """Rows of K and of V are written by different threads: in one cache their order would be left to chance."""
+    d = _desc()
+    assert _evict(d, k=A, v=A) == tv.TV_ERR_INVALID_ARG
+    assert _rotary(d, _rot(), ck=A, cv=A) == tv.TV_ERR_INVALID_ARG
+    assert _rotary(d, _rot(), q=None, qo=None, ck=A, cv=A) == tv.TV_ERR_INVALID_ARG
+
+
+def test_writers_refuse_bad_arguments_with_two_caches():
+    """Each refusal by itself, not for the caches' being one."""
+    two = dict(k=A, v=3 * A)
+    for kw, status in BAD_DESCS:
+        d = _desc(**kw)
+        assert _evict(d, **two) == status
+        assert _rotary(d, _rot(rotary_dim=min(128, max(16, d.head_dim))), cv=3 * A) == status
+    d = _desc()
+    for kw in (dict(budget=0), dict(sink=-1), dict(recent=-1), dict(budget=8, sink=4, recent=5),
+               dict(table=None), dict(lens=None), dict(w=None), dict(kept=None), dict(new=None), dict(new=A),
+               dict(k=None), dict(v=None), dict(k=A + 8), dict(v=A + 8), dict(dst=A)):
+        assert _evict(d, **{**two, **kw}) == tv.TV_ERR_INVALID_ARG
+    for kw in (dict(k=None), dict(v=None), dict(f=None), dict(pre=None), dict(table=None), dict(ck=None), dict(q=None),
+               dict(qo=None), dict(q=A + 8), dict(k=A + 8), dict(v=A + 8), dict(qo=A + 8), dict(ck=A + 8)):
+        assert _rotary(d, _rot(), cv=3 * A, **kw) == tv.TV_ERR_INVALID_ARG
+    for kw in (dict(num_nodes=0), dict(rotary_dim=0), dict(rotary_dim=144), dict(interleaved=2), dict(num_axes=0),
+               dict(q_stride=1016), dict(k_stride=260), dict(v_stride=128)):
+        assert _rotary(d, _rot(**kw), cv=3 * A) == tv.TV_ERR_INVALID_ARG
+    assert _rotary(d, _rot(q_stride=2048), q=A, qo=A, cv=3 * A) == tv.TV_ERR_INVALID_ARG
+
+
 def test_references_against_closed_forms():
     c = Cache(0, [1, 40], 2, 64, "f32")
     q = as_type(c.rng.standard_normal((2, 4, 64)), "f32")

@@ -543,6 +543,8 @@ tv_status tv_evict_cache(const tv_cache_desc* desc, int32_t budget, int32_t sink
     if (budget > INT32_MAX / 2) return TV_ERR_UNSUPPORTED;
     const int64_t most = budget < max_len ? budget : max_len;  // rows of a head; a CTA moves at least 32
     if ((int64_t)desc->batch * desc->num_kv_heads * (most / 32 + 16) * 2 > INT32_MAX) return TV_ERR_UNSUPPORTED;
+    // K and V rows are moved by different CTAs: in one cache, a row could be moved twice
+    if (!dst_block_table && paged_k == paged_v) return TV_ERR_INVALID_ARG;
     tv::EvictArgs a = {};
     a.k = paged_k; a.v = paged_v; a.c = cache_view(desc, block_table); a.dst_table = dst_block_table;
     a.lens = kv_lens; a.weights = weights; a.weights_out = weights_out; a.kept = kept; a.new_lens = new_kv_lens;
@@ -578,6 +580,7 @@ tv_status tv_rotary_write(const tv_cache_desc* desc, const tv_rotary_desc* rot, 
         misaligned(paged_v))
         return TV_ERR_INVALID_ARG;
     if (q && q == q_out && qs != qrow) return TV_ERR_INVALID_ARG;
+    if (paged_k == paged_v) return TV_ERR_INVALID_ARG;  // a row would get its key or its value
     tv::RotaryArgs a = {};
     a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.cache_k = paged_k; a.cache_v = paged_v;
     a.c = cache_view(desc, block_table);
