@@ -555,10 +555,14 @@ typedef struct {
  *                of a row is left as it was.  What tv_evict_cache reads.
  * Query head h reads KV head h / (num_q_heads / num_kv_heads).  Arithmetic is
  * fp32; for bf16 and fp16 the softmax weights enter the product with the
- * values as two 16-bit parts, so only `out` itself is rounded.
+ * values as two 16-bit parts, which leave out less than 2^-16 of a bf16 weight
+ * (less of an fp16 one), and `out` is rounded once.
  * A sequence with kv_lens[b] = 0 (padding of a batch) gets zeros and an lse
- * of -inf, as does a row whose scores are all -inf; a NaN score makes its row NaN
- * (out, lse, and the weights of its KV head).  A length outside
+ * of -inf, as does a row whose scores are all -inf; a score of NaN or +inf makes its
+ * row NaN (out, lse, and the weights of its KV head).  A NaN or an infinity in V
+ * reaches that element of the KV head's outputs alone: NaN for a NaN; for an infinity
+ * the infinity in fp32, and in bf16 and fp16 it or NaN (the products of the two
+ * parts need not agree).  A length outside
  * [0, max_kv_len] or a block id out of range gives the sequence NaN rows, leaves
  * its attn_weights as they were and writes TV_ERR_INVALID_ARG or
  * TV_ERR_BLOCK_TABLE to *dev_status.  Cache slots past kv_lens[b] are not read.

@@ -68,3 +68,47 @@ def test_a_dirty_workspace_and_what_lies_behind_it(lens, hkv, g, d, dtype, weigh
     assert not (ws[:size] == 0xff).all()
     with pytest.raises(tv.TreeVerifyError):
         tv.decode_attention(*args, attn_weights=dw, out=out, lse=lse, workspace=ws[:size - 256])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", [[40], [6000]])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_values_that_are_not_finite(dtype, lens, value):
+    """One element of one value row: that element of the head's outputs is not finite (in fp32 as the
+    definition gives it), everything else stays as it was."""
+    c = Cache(31, lens, 2, 64, dtype)
+    q, _ = _inputs(c, 4, as_type(0.5 * c.rng.standard_normal((1, 4, 64)), dtype))  # no weight underflows
+    w = np.zeros((1, 2, c.width * 16), np.float32)
+    ref, tol = decode_reference(c, q, w)
+    for t in (0, lens[0] // 2, lens[0] - 1):
+        at = (c.table[0, t // 16], t % 16, 1, 7)
+        keep, c.v[at] = c.v[at], value
+        _, args = _inputs(c, 4, q)
+        dw = to_gpu(w)
+        out, lse = tv.decode_attention(*args, attn_weights=dw)
+        c.v[at] = keep
+        hit = out[0, 2:, 7].float().cpu().numpy()  # the two query heads of KV head 1
+        assert not np.isfinite(hit).any()
+        if dtype == "f32" and not np.isnan(value):
+            assert (hit == value).all()
+        if np.isnan(value):
+            assert np.isnan(hit).all()
+        out[0, 2:, 7] = to_gpu(ref[0][0, 2:, 7]).to(out.dtype)
+        _within(out, ref[0], tol[0], "out")
+        _within(lse, ref[1], tol[1], "lse")
+        _within(dw, ref[2], tol[2], "weights")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", [[40, 21], [6000, 21]])
+def test_an_infinite_score_makes_its_row_nan(dtype, lens):
+    c = Cache(32, lens, 1, 64, dtype)
+    q = as_type(c.rng.standard_normal((2, 2, 64)), dtype)
+    q[0, :, 0] = 1
+    c.k[c.table[0, 1], 3, 0, 0] = np.inf
+    w = np.zeros((2, 1, c.width * 16), np.float32)
+    _, args = _inputs(c, 2, q)
+    dw = to_gpu(w)
+    out, lse = tv.decode_attention(*args, attn_weights=dw)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all() and torch.isnan(dw[0, 0, :lens[0]]).all()
+    assert torch.isfinite(out[1]).all() and torch.isfinite(lse[1]).all() and torch.isfinite(dw[1]).all()
