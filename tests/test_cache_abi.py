@@ -296,6 +296,42 @@ def test_writers_refuse_bad_arguments_with_two_caches():
     assert _rotary(d, _rot(q_stride=2048), q=A, qo=A, cv=3 * A) == tv.TV_ERR_INVALID_ARG
 
 
+def test_every_wrapper_checks_the_caches_alike():
+    """Types, shapes, strides and overlaps of the caches and the table, through each call that takes them."""
+    c = torch.zeros(4, 16, 2, 64)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    heads_first = c.transpose(1, 2).contiguous().transpose(1, 2)
+    calls = [
+        lambda k, v, t: tv.cache_desc(k, v, t, 4),
+        lambda k, v, t: tv.decode_attention(torch.zeros(1, 4, 64, dtype=k.dtype), k, v, t, lens),
+        lambda k, v, t: tv.evict_cache(k, v, t, lens, torch.zeros(1, 2, 32), 8),
+        lambda k, v, t: tv.rotary_write(*[torch.zeros(1, 1, 2, 64, dtype=k.dtype)] * 2, torch.ones(32), k, v, t, lens),
+    ]
+    last = torch.zeros(4, 16, 2, 128)[..., ::2]
+    bad = [(c.double(), c.double(), table, TypeError, "dtype"), (c, c[:3], table, TypeError, "one type"),
+           (c, c.half(), table, TypeError, "one type"), (c[0], c[0], table, TypeError, "one type"),
+           (c, c, table.long(), TypeError, "block_table"), (c, c, table[0], TypeError, "block_table"),
+           (c, c, table.expand(3, 2)[:, :1], TypeError, "block_table"),
+           (c[:1].expand(4, 16, 2, 64), c[:1].expand(4, 16, 2, 64), table, ValueError, "k_cache: rows overlap"),
+           (c, c[:, :1].expand(4, 16, 2, 64), table, ValueError, "v_cache: rows overlap"),
+           (c[:, :, :1].expand(4, 16, 2, 64), c, table, ValueError, "k_cache: rows overlap"),
+           (c, heads_first, table, ValueError, "same strides"), (last, last, table, ValueError, "contiguous")]
+    for call in calls:
+        for k, v, t, error, match in bad:
+            with pytest.raises(error, match=match):
+                call(k, v, t)
+    for k in (c, heads_first):
+        for call in calls[1:]:
+            with pytest.raises(ValueError, match="CUDA"):
+                call(k, k, table)
+    d = tv.cache_desc(heads_first, heads_first, table, softmax_scale=0.5, max_kv_len=7)
+    assert (d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.block_size, d.max_blocks_per_seq, d.num_blocks,
+            d.dtype, d.softmax_scale, d.max_kv_len) == (1, 2, 2, 64, 16, 2, 4, tv.TV_F32, 0.5, 7)
+    for kw in (dict(num_q_heads=-1), dict(num_q_heads=1 << 40), dict(max_kv_len=1 << 40)):
+        with pytest.raises(ValueError, match="range"):
+            tv.cache_desc(c, c, table, **kw)
+
+
 def test_references_against_closed_forms():
     c = Cache(0, [1, 40], 2, 64, "f32")
     q = as_type(c.rng.standard_normal((2, 4, 64)), "f32")

@@ -533,7 +533,7 @@ _calls = None
 
 
 def _native():
-    """The marshalling module of the three calls below; raises if it has not been built."""
+    """The marshalling module of the calls below; raises if it has not been built."""
     global _calls
     if _calls is None:
         lib()
@@ -548,48 +548,13 @@ def _native():
     return _calls
 
 
-_cache_types: dict = {}
-
-
 def cache_desc(k_cache, v_cache, block_table, num_q_heads: int | None = None, softmax_scale: float = 0.0,
                max_kv_len: int = 0) -> TvCacheDesc:
     """Descriptor of a paged cache from tensors: caches [nb][block][Hkv][D] of any
     strides with contiguous head rows (equal for K and V), block_table [B][max_blocks]
     int32."""
-    import torch
-    if not _cache_types:
-        _cache_types.update({torch.bfloat16: TV_BF16, torch.float32: TV_F32, torch.float16: TV_F16})
-    dt = _cache_types.get(k_cache.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {k_cache.dtype}")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must be [num_blocks][block_size][num_kv_heads][head_dim] of one type")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
-        raise TypeError("block_table must be a contiguous int32 [batch][max_blocks]")
-    nb, bs, hkv, d = k_cache.shape
-    strides = (0, 0, 0)
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        strides = _row_strides("k_cache", k_cache)
-        if _row_strides("v_cache", v_cache) != strides:
-            raise ValueError("k_cache and v_cache must have the same strides")
-    b, mb = block_table.shape
-    return TvCacheDesc(b, hkv if num_q_heads is None else num_q_heads, hkv, d, bs, mb, nb, dt, float(softmax_scale),
-                       int(max_kv_len), *strides, 0, 0)
-
-
-def _row_strides(name, c):
-    """Strides of the first three dimensions of a cache (those of dimensions of size 1 say
-    nothing: the row's); the last has to be 1, and no two rows may share memory."""
-    if c.stride(3) != 1 and c.size(3) > 1:
-        raise ValueError(f"{name}: the elements of a head's row must be contiguous")
-    strides = tuple(st if n > 1 else c.size(3) for n, st in zip(c.shape[:3], c.stride()[:3]))
-    end = c.size(3)
-    for st, n in sorted(zip(strides, c.shape[:3])):
-        if n > 1:
-            if st < end:
-                raise ValueError(f"{name}: rows overlap (strides {tuple(c.stride())})")
-            end = st * (n - 1) + end
-    return strides
+    return TvCacheDesc.from_buffer_copy(_native().cache_desc(k_cache, v_cache, block_table, num_q_heads, softmax_scale,
+                                                             max_kv_len))
 
 
 def decode_attention(q, k_cache, v_cache, block_table, kv_lens, softmax_scale: float = 0.0, attn_weights=None,

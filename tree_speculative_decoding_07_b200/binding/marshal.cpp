@@ -180,7 +180,7 @@ void row_strides(const char* name, const at::Tensor& c, int64_t (&s)[3]) {
         }
 }
 
-tv_cache_desc cache_desc(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, int64_t heads, float scale,
+tv_cache_desc describe(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, int64_t heads, float scale,
                          int64_t max_kv_len) {
     tv_cache_desc d = {};
     switch (k.scalar_type()) {
@@ -233,6 +233,15 @@ PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
     return r;
 }
 
+// (k_cache, v_cache, block_table, num_q_heads or None, softmax_scale, max_kv_len) -> the descriptor's bytes; the
+// tensors may lie anywhere
+PyObject* cache_desc(Args a) {
+    const at::Tensor &k = *a.tensor(0, "k_cache"), &v = *a.tensor(1, "v_cache"), &table = *a.tensor(2, "block_table");
+    const int64_t heads = a.v[3] == Py_None ? -1 : a.integer(3, "num_q_heads", 0);
+    const tv_cache_desc d = describe(k, v, table, heads, a.real(4), a.integer(5, "max_kv_len"));
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&d), sizeof d);
+}
+
 // (q, k_cache, v_cache, block_table, kv_lens, softmax_scale, attn_weights, out, lse, workspace, max_kv_len,
 //  dev_status, stream) -> (out, lse)
 PyObject* decode_attention(Args a) {
@@ -244,7 +253,7 @@ PyObject* decode_attention(Args a) {
     if (q.dim() != 3 || q.scalar_type() != k.scalar_type())
         type_error("q must be [batch][heads][head_dim] of the caches' type");
     const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2);
-    tv_cache_desc d = cache_desc(k, v, table, Hq, a.real(5), a.integer(10, "max_kv_len"));
+    tv_cache_desc d = describe(k, v, table, Hq, a.real(5), a.integer(10, "max_kv_len"));
     if (d.batch != B || d.head_dim != D) value_error("q, block_table and the caches disagree on batch or head_dim");
     if (!q.is_contiguous()) {
         if ((D > 1 && q.stride(2) != 1) || (Hq > 1 && q.stride(1) != D))
@@ -285,7 +294,7 @@ PyObject* evict_cache(Args a) {
     const at::Tensor *dst = a.tensor(8, "dst_block_table", true), *wo = a.tensor(9, "weights_out", true);
     const at::Tensor *kept_p = a.tensor(10, "kept", true), *new_p = a.tensor(11, "new_kv_lens", true);
     const at::Tensor* status = a.tensor(13, "dev_status", true);
-    tv_cache_desc d = cache_desc(k, v, table, -1, 0.f, a.integer(12, "max_kv_len"));
+    tv_cache_desc d = describe(k, v, table, -1, 0.f, a.integer(12, "max_kv_len"));
     const int64_t B = d.batch, H = d.num_kv_heads, budget = a.integer(5, "budget");
     const int64_t sink = a.integer(6, "sink"), recent = a.integer(7, "recent");
     want("kv_lens", lens, at::kInt, {B});
@@ -339,7 +348,7 @@ PyObject* rotary_write(Args a) {
         Hq = q->size(2);
         r.q_stride = node_stride("q", *q);
     }
-    tv_cache_desc d = cache_desc(ck, cv, table, Hq, 0.f, 0);
+    tv_cache_desc d = describe(ck, cv, table, Hq, 0.f, 0);
     if (d.batch != B || d.num_kv_heads != H || d.head_dim != D)
         value_error("k, block_table and the caches disagree on batch, heads or head_dim");
     const int64_t pairs = freq.numel();
@@ -409,7 +418,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 
 #define FAST(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    FAST(decode_attention, 13), FAST(evict_cache, 15), FAST(rotary_write, 17),
+    FAST(decode_attention, 13), FAST(evict_cache, 15), FAST(rotary_write, 17), FAST(cache_desc, 6),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
