@@ -517,7 +517,7 @@ tv_status tv_decode_attention(const tv_cache_desc* desc, const void* q, const vo
     a.part_o = reinterpret_cast<float*>(ws + y.o);
     a.scores = reinterpret_cast<float*>(ws + y.scores);
     a.B = desc->batch; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads; a.G = a.Hq / a.Hkv;
-    a.D = desc->head_dim; a.HT = y.plan.HT; a.GS = y.plan.GS; a.NG = y.plan.NG; a.grid = y.plan.grid;
+    a.D = desc->head_dim; a.GS = y.plan.GS; a.NG = y.plan.NG; a.grid = y.plan.grid;
     a.max_len = cache_max_len(desc);
     a.cap_tiles = (a.max_len + 15) / 16;
     const float scale = desc->softmax_scale > 0.f ? desc->softmax_scale : 1.0f / sqrtf((float)desc->head_dim);
@@ -588,7 +588,7 @@ tv_status tv_rotary_write(const tv_cache_desc* desc, const tv_rotary_desc* rot, 
     a.parent = positions ? nullptr : parent_idx; a.counts = rot->node_counts; a.status = dev_status;
     a.q_stride = qs; a.k_stride = ks; a.v_stride = vs;
     a.B = desc->batch; a.N = rot->num_nodes; a.Hq = desc->num_q_heads; a.Hkv = desc->num_kv_heads;
-    a.D = desc->head_dim; a.rot = rot->rotary_dim; a.interleaved = rot->interleaved; a.axes = rot->num_axes;
+    a.D = desc->head_dim; a.rot = rot->rotary_dim; a.interleaved = rot->interleaved;
     for (int i = 0; i < rot->rotary_dim / 2; ++i) a.axis_of_pair[i] = rot->axis_of_pair[i];
     return tv::launch_rotary(a, desc->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }

@@ -162,7 +162,7 @@ struct DecodeArgs {
     float2* part_ml;       // [2 * grid][HT] running maximum and sum of the pieces
     float* part_o;         // [2 * grid][HT][D] their unnormalised outputs
     float* scores;         // [tile][16][GS] scaled scores, log2 domain (with weights)
-    int B, Hq, Hkv, G, D, HT, GS, NG, max_len, grid;
+    int B, Hq, Hkv, G, D, GS, NG, max_len, grid;
     int cap_tiles;         // 16-token tiles of max_len
     float scale_log2;
 };
@@ -191,7 +191,7 @@ struct RotaryArgs {
     const int32_t* counts;          // [B] or NULL
     int32_t* status;
     int64_t q_stride, k_stride, v_stride;  // elements between consecutive nodes
-    int B, N, Hq, Hkv, D, rot, interleaved, axes;
+    int B, N, Hq, Hkv, D, rot, interleaved;
     uint8_t axis_of_pair[128];
 };
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st);
