@@ -52,12 +52,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Needs libtreeverify.so (it is linked to it) and torch's headers and libraries."""
+def marshal_unavailable() -> str | None:
+    """Why the marshalling module cannot be compiled here, or None."""
+    cxx = os.environ.get("CXX", "g++")
+    if shutil.which(cxx) is None:
+        return f"no C++ compiler ({cxx})"
+    try:
+        import torch
+    except ImportError as e:
+        return f"no torch ({e})"
+    for d, name in ((os.path.join(os.path.dirname(torch.__file__), "include"), "ATen/core/Tensor.h"),
+                    (sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(os.path.join(d, name)):
+            return f"no {name} in {d}"
+    return None
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
+    """Needs libtreeverify.so (it is linked to it), a C++ compiler and the headers of torch and Python.  Where one of
+    those is missing it says so and returns None: then everything but the wrappers of the cache calls works, and
+    those raise."""
+    why = marshal_unavailable()
+    if why is not None:
+        print(f"_marshal.so not built: {why}; decode_attention, evict_cache, rotary_write and cache_desc need it",
+              file=sys.stderr)
+        return None
+    import torch
     deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "treeverify.h")]
     if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
         return MARSHAL
-    import torch
     base = os.path.dirname(torch.__file__)
     nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
