@@ -543,6 +543,10 @@ def _native():
         except ImportError as e:
             raise ImportError(f"_marshal.so not built in {_HERE} ({e}); run __graft_entry__.build() or python -m "
                               "tree_speculative_decoding_07_b200.build_lib") from e
+        from .build_lib import marshal_target
+        if _marshal.built_for != marshal_target():
+            raise ImportError(f"_marshal.so in {_HERE} was built for {_marshal.built_for}, this is {marshal_target()}; "
+                              "run python -m tree_speculative_decoding_07_b200.build_lib")
         _marshal.set_error(TreeVerifyError)
         _calls = _marshal
     return _calls

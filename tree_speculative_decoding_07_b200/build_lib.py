@@ -26,6 +26,7 @@ NVCC_FLAGS = [
 
 MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_STAMP = os.path.join(PKG, "_marshal.built_for")
 
 
 def sources():
@@ -50,6 +51,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     return LIB
+
+
+def marshal_target() -> str:
+    """What a marshalling module is compiled for: another torch or Python needs another one."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
 
 
 def marshal_unavailable() -> str | None:
@@ -79,13 +86,18 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
         return None
     import torch
     deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "treeverify.h")]
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+    target = marshal_target()
+    built_for = None
+    if os.path.exists(MARSHAL) and os.path.exists(MARSHAL_STAMP):
+        with open(MARSHAL_STAMP) as f:
+            built_for = f.read()
+    if not force and built_for == target and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
         return MARSHAL
     base = os.path.dirname(torch.__file__)
     nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{target}"',
            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
@@ -93,7 +105,11 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
+    if os.path.exists(MARSHAL_STAMP):  # no module of an unfinished build passes for this one's
+        os.remove(MARSHAL_STAMP)
     subprocess.check_call(cmd)
+    with open(MARSHAL_STAMP, "w") as f:
+        f.write(target)
     return MARSHAL
 
 
