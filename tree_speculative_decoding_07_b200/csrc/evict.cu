@@ -440,8 +440,8 @@ int evict_max_len() { return SE_MAX_CLUSTER * SE_MAX_SLICE; }
 
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t st) {
     const int heads = a.B * a.Hkv;
-    // Slices of 2,048 sums (four for each thread), as long as the GPU holds twice the CTAs at
-    // four per SM.  At 128K sums and 8 heads clusters of 4, 8 and 16 took (with the move) 63, 50
+    // Slices of 2,048 to 4,096 sums (four to eight for each thread), as long as the GPU holds twice
+    // the CTAs at four per SM.  At 128K sums and 8 heads clusters of 4, 8 and 16 took (with the move) 63, 50
     // and 49 us; above 8, which not every part of the GPU can place, only for what would not fit.
     int C = 1;
     while (C < 8 && (int64_t)C * 4096 < a.max_len && (int64_t)heads * C * 2 <= 4 * sms) C *= 2;
